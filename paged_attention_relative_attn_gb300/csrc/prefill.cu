@@ -69,6 +69,7 @@ constexpr int kBiasPitch = 68;                       // floats per row band (64 
 constexpr int kBiasWarpBytes = 32 * kBiasPitch * 4;  // 32 rows of one warp
 constexpr int kBiasBufBytes = 4 * kBiasWarpBytes;    // 128 rows
 constexpr float kRescaleThreshold = 8.0f;            // log2 units: rescale O when max grows > 2^8
+constexpr float kBigScore = 0x1p20f;                 // fp32 holds m log2 e to 2^-4 up to here
 
 struct PrefillParams {
   CUtensorMap tmap_q[4];    // tokens r + 4y of q: {D, H_q, y}, box {64, 1, 32}
@@ -681,7 +682,20 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       l_part *= alpha;
       const float nmu = (m_use == -INFINITY) ? 0.f : -m_use * kLog2e;
       uint32_t pk[16];
-      {
+      // 2^(s log2 e - m log2 e) in one fma, or, where m is so large that the
+      // rounding of m log2 e counts (masks such as -1e9 or fp32's lowest value
+      // on every key so far), from the difference s - m
+      if (__any_sync(0xffffffffu, fabsf(m_use) > kBigScore && m_use > -INFINITY)) {
+        const float base = m_use == -INFINITY ? 0.f : m_use;
+        float u = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+          const float p0 = ex2((s[2 * m] - base) * kLog2e), p1 = ex2((s[2 * m + 1] - base) * kLog2e);
+          u += p0 + p1;
+          pk[m] = pack_bf16(p0, p1);
+        }
+        l_part += u;
+      } else {
         const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), nmu2 = f2_pack(nmu, nmu);
         uint64_t acc[4] = {0, 0, 0, 0};  // four packed partial sums (+0.0 bits)
 #pragma unroll
