@@ -67,6 +67,7 @@ extern "C" {
 #define INKLING_DEVERR_TIMEOUT 4     /* a pipeline wait gave up; outputs are invalid */
 #define INKLING_DEVERR_BAD_CHUNK 8   /* prefill: q_len > seq_len or q_len > max_q_len */
 #define INKLING_DEVERR_BAD_SLOT 16   /* kv_conv_append: state pool row out of range */
+#define INKLING_DEVERR_NO_PAGES 32   /* build_tables: the free list cannot serve a request */
 
 /*
  * inkling_rel_attn_decode -- one query token per sequence.
@@ -299,6 +300,158 @@ int inkling_rel_attn_kv_conv_append(
     int32_t max_q_len, int32_t H_kv, int32_t D, int32_t page_size,
     int32_t num_pages, void* k_cache, void* v_cache, int32_t* device_error,
     void* stream);
+
+/*
+ * inkling_rel_attn_build_tables -- the tables of one serving step, built on
+ * the GPU from request lengths: lengths after the step, where each request's
+ * new tokens start, its page-table entries, and the cache slot of each new
+ * token.  Request b holds seq_lens[b] tokens in the pages its page-table row
+ * lists and asks for new_lens[b]:
+ *   >= 0  that many new tokens (0: none in this step).  It takes
+ *         ceil((seq_lens + new) / page_size) - ceil(seq_lens / page_size) pages
+ *         from the free list; they become the next entries of its row.
+ *   <  0  it has ended: the pages of its row go back to the free list.
+ * The free list is a stack, free_pages[0 .. *free_count - 1].  Ended requests'
+ * pages are put on top first, in batch order and each row in page order;
+ * then pages are taken from the top, in batch order.  A request needing pages
+ * is served iff the pages asked for by it and by all requests before it are
+ * there; otherwise it is refused (INKLING_DEVERR_NO_PAGES), as is one whose row
+ * cannot hold it (INKLING_DEVERR_SEQ_TOO_LONG; it takes no pages): its length
+ * and row stay as they were and its new tokens get slot -1, so its outputs
+ * of this step are to be ignored and it can ask again.
+ *
+ *   seq_lens      int32 [B], tokens held;  new_lens int32 [B]
+ *   page_table    int32 [B, page_table_stride], rows of served requests extended
+ *                 in place; no other entry is written
+ *   free_pages    int32 [num_pages], returned pages written above the top;
+ *                 free_count int32 [1]
+ *   kv_lens       int32 [B], out: seq_lens + new_lens (0: ended; refused:
+ *                 unchanged).  May be seq_lens itself
+ *   cu_seqlens_q  int32 [B + 1], out: prefix sums of max(new_lens, 0), refused
+ *                 requests counted -- the packing of the step's rows
+ *   slot_map      int64 [max_tokens], out: page * page_size + place of packed
+ *                 token t; -1 for a refused request's tokens and for
+ *                 t >= cu_seqlens_q[B].  May be NULL when max_tokens is 0
+ *   free_left     int32 [1], out: the stack's height.  May be free_count itself
+ * With separate outputs the call leaves its inputs as they are but for entries
+ * above them, so it may be repeated; with kv_lens = seq_lens and free_left =
+ * free_count it steps the state in place, in a captured graph too.  Page ids
+ * outside [0, num_pages) on the stack set INKLING_DEVERR_BAD_PAGE and give slot
+ * -1, and so does a stack that would grow past num_pages (the pages past it are
+ * dropped); more new tokens than max_tokens set INKLING_DEVERR_BAD_CHUNK (the
+ * tokens past it get no slot).  B <= 8192, page_size as everywhere.
+ */
+int inkling_rel_attn_build_tables(
+    const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_table,
+    int32_t page_table_stride, int32_t* free_pages, const int32_t* free_count,
+    int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
+    int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
+    int32_t* free_left, int32_t* device_error, void* stream);
+
+/*
+ * The 4-bit cache
+ * ---------------
+ * The entry points named *_q4 work on K and V pools held in 4 bits, paged like
+ * the bf16 ones: uint8 [num_pages][H_kv][page_size * 9 * D / 16], 144 bytes per
+ * token and KV head for D = 128, K and V together (512 in bf16).  A row (a
+ * token's D channels of one KV head) is cut into groups of 32 adjacent
+ * channels.  A group with the largest magnitude a holds
+ *   s = a / 7 rounded up to 5 significant bits, as a bf16 number,
+ *   x = v / s rounded to the nearest integer, ties toward zero (|x| <= 7),
+ * and stands for x * s -- always a bf16 number, so reading a row back rounds
+ * nothing.  A group with a < 2^-100 holds zeros; magnitudes above 2^127, infinities
+ * too, count as 2^127; a group with a NaN reads as NaN.
+ *   Within one (page, KV head) tokens come in blocks of 16: 16 rows of D / 2
+ * bytes (place p of the block at p * D / 2), then 16 rows of D / 32 scales.  The
+ * nibbles hold x + 8 in the order the attention's matrix instructions read
+ * them: with N = D / 32 and group j, 32-bit word N * t + j of a K row holds the
+ * channels 32 j + 8 t + 0 .. 7 and 16-bit unit N * g + j of a V row the channels
+ * 32 j + 4 g + 0 .. 3, lowest nibble first.  D in {64, 128}; pools 16-byte aligned.
+ */
+
+/*
+ * inkling_rel_attn_kv_append_q4 -- quantise the new tokens' K and V rows into
+ * the 4-bit cache (the counterpart of inkling_rel_attn_kv_append).
+ *
+ *   k_new, v_new  bf16 [T, H_kv, D], 16-byte aligned
+ *   slot_map      int64 [T]: token t goes to page slot_map[t] / page_size, place
+ *                 slot_map[t] % page_size (inkling_rel_attn_build_tables makes
+ *                 it).  Negative: the token is skipped.  Past the pool:
+ *                 INKLING_DEVERR_BAD_PAGE, skipped.  Slots of one call must be
+ *                 distinct (two tokens of one slot leave a mixture of both)
+ * No other byte of the cache is written.
+ */
+int inkling_rel_attn_kv_append_q4(
+    const void* k_new, const void* v_new, const int64_t* slot_map, int32_t T,
+    int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    void* k_cache, void* v_cache, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_kv_read_q4 -- rows of the 4-bit cache as the bf16 values they
+ * stand for: k_rows, v_rows bf16 [T, H_kv, D] from the slots slot_map[t] (zeros
+ * for a negative slot; past the pool zeros and INKLING_DEVERR_BAD_PAGE).  Slots
+ * may repeat.
+ */
+int inkling_rel_attn_kv_read_q4(
+    const int64_t* slot_map, const void* k_cache, const void* v_cache,
+    int32_t T, int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    void* k_rows, void* v_rows, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_decode_q4 -- inkling_rel_attn_decode_multi over the 4-bit
+ * cache: the last q_len (1 .. 64) tokens of each sequence, q_len = 1 being plain
+ * decode.  Same formula on the values x * s, same shapes, lengths and errors;
+ * one more rule: a row all of whose visible scores are -inf gets out = 0, lse =
+ * -inf.  Keys past a row's position or window, and places past a sequence's
+ * end, may hold any bytes.
+ *   The work is cut over the GPU by the batch's lengths, read on the device:
+ * no host bound on them is needed, and results do not depend on page ids or
+ * timing (they do depend, in the last bits, on the other lengths in the batch).
+ *   workspace  inkling_rel_attn_decode_q4_workspace_size bytes, 16-byte aligned,
+ *              no content expected or kept; calls that may overlap need one each
+ */
+int inkling_rel_attn_decode_q4(
+    const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* page_table, int32_t page_table_stride,
+    const int32_t* seq_lens, const float* rel_logits, int32_t B, int32_t q_len,
+    int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    int32_t R, int32_t window, float scale, void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes, int32_t* device_error,
+    void* stream);
+
+/* Workspace bytes of inkling_rel_attn_decode_q4 for these scalars (0: none
+ * needed).  Host only; num_sms as for inkling_rel_attn_decode_workspace_size. */
+size_t inkling_rel_attn_decode_q4_workspace_size(int32_t B, int32_t q_len,
+                                                 int32_t H_q, int32_t H_kv,
+                                                 int32_t D, int32_t num_sms);
+
+/*
+ * inkling_rel_attn_prefill_q4 -- inkling_rel_attn_prefill over the 4-bit cache:
+ * same arguments, formula and errors.  The keys that a sequence's chunk sees are
+ * first expanded into bf16 pages in the workspace, then attended to, so
+ * the workspace holds min(max_seq_len, window + max_q_len + 62) tokens of every
+ * sequence (max_seq_len when window <= 0), 4 * H_kv * D bytes each.
+ *   max_seq_len  bound on seq_lens: a sequence whose visible keys do not fit the
+ *                workspace sets INKLING_DEVERR_SEQ_TOO_LONG and
+ *                INKLING_DEVERR_BAD_CHUNK and is skipped
+ *   workspace    inkling_rel_attn_prefill_q4_workspace_size bytes, 256-byte
+ *                aligned, no content expected or kept; calls that may overlap
+ *                need one each
+ */
+int inkling_rel_attn_prefill_q4(
+    const void* q, const int32_t* cu_seqlens_q, const void* k_cache,
+    const void* v_cache, const int32_t* page_table, int32_t page_table_stride,
+    const int32_t* seq_lens, const float* rel_logits, int32_t B, int32_t T,
+    int32_t max_q_len, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+    int32_t num_pages, int32_t R, int32_t window, float scale,
+    int32_t max_seq_len, void* out, float* lse_out, void* workspace,
+    size_t workspace_bytes, int32_t* device_error, void* stream);
+
+/* Workspace bytes of inkling_rel_attn_prefill_q4 for these scalars.  Host only. */
+size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len,
+                                                  int32_t H_kv, int32_t D,
+                                                  int32_t window,
+                                                  int32_t max_seq_len);
 
 /*
  * inkling_rel_attn_choose_splits -- the decode split count, a pure host

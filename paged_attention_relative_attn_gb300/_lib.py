@@ -23,6 +23,13 @@ EXPORTED = (
     "inkling_rel_attn_prefill",
     "inkling_rel_attn_kv_append",
     "inkling_rel_attn_kv_conv_append",
+    "inkling_rel_attn_build_tables",
+    "inkling_rel_attn_kv_append_q4",
+    "inkling_rel_attn_kv_read_q4",
+    "inkling_rel_attn_decode_q4",
+    "inkling_rel_attn_decode_q4_workspace_size",
+    "inkling_rel_attn_prefill_q4",
+    "inkling_rel_attn_prefill_q4_workspace_size",
     "inkling_rel_attn_choose_splits",
     "inkling_rel_attn_decode_workspace_size",
     "inkling_rel_attn_prefill_workspace_size",
@@ -69,6 +76,28 @@ _SIGS = {
         _p, _p, _i32, _p, _p, _p, _i32,             # w_k w_v width state_k state_v slots num_slots
         _i32, _i32, _i32, _i32, _i32, _i32, _i32,   # B T max_q_len H_kv D page_size num_pages
         _p, _p, _p, _p]),                           # k_cache v_cache err stream
+    "inkling_rel_attn_build_tables": (ctypes.c_int, [
+        _p, _p, _p, _i32, _p, _p,                   # seq_lens new_lens page_table stride free count
+        _i32, _i32, _i32, _i32,                     # B page_size num_pages max_tokens
+        _p, _p, _p, _p, _p, _p]),                   # kv_lens cu slot_map free_left err stream
+    "inkling_rel_attn_kv_append_q4": (ctypes.c_int, [
+        _p, _p, _p, _i32, _i32, _i32, _i32, _i32,   # k_new v_new slot_map T H_kv D page_size num_pages
+        _p, _p, _p, _p]),                           # k_cache v_cache err stream
+    "inkling_rel_attn_kv_read_q4": (ctypes.c_int, [
+        _p, _p, _p, _i32, _i32, _i32, _i32, _i32,   # slot_map k_cache v_cache T H_kv D page_size num_pages
+        _p, _p, _p, _p]),                           # k_rows v_rows err stream
+    "inkling_rel_attn_decode_q4": (ctypes.c_int, [
+        _p, _p, _p, _p, _i32, _p, _p,               # q k v page_table stride seq_lens rel
+        _i32, _i32, _i32, _i32, _i32, _i32, _i32,   # B q_len H_q H_kv D page_size num_pages
+        _i32, _i32, _f32,                           # R window scale
+        _p, _p, _p, _sz, _p, _p]),                  # out lse ws ws_bytes err stream
+    "inkling_rel_attn_decode_q4_workspace_size": (_sz, [_i32] * 6),
+    "inkling_rel_attn_prefill_q4": (ctypes.c_int, [
+        _p, _p, _p, _p, _p, _i32, _p, _p,           # q cu k v page_table stride seq_lens rel
+        _i32, _i32, _i32, _i32, _i32, _i32, _i32,   # B T max_q_len H_q H_kv D page_size
+        _i32, _i32, _i32, _f32, _i32,               # num_pages R window scale max_seq_len
+        _p, _p, _p, _sz, _p, _p]),                  # out lse ws ws_bytes err stream
+    "inkling_rel_attn_prefill_q4_workspace_size": (_sz, [_i32] * 6),
     "inkling_rel_attn_choose_splits": (_i32, [_i32, _i32, _i32, _i32, _i32]),
     "inkling_rel_attn_decode_workspace_size": (_sz, [_i32] * 8),
     "inkling_rel_attn_prefill_workspace_size": (_sz, [_i32] * 3),
@@ -169,6 +198,58 @@ def inkling_rel_attn_kv_conv_append(k_new, v_new, cu_seqlens_q, seq_lens, page_t
         _v(conv_w_k), _v(conv_w_v), width, _v(conv_state_k), _v(conv_state_v), _v(state_slots),
         num_slots, B, T, max_q_len, H_kv, D, page_size, num_pages, _v(k_cache), _v(v_cache),
         _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_build_tables(seq_lens, new_lens, page_table, page_table_stride, free_pages,
+                                  free_count, B, page_size, num_pages, max_tokens, kv_lens,
+                                  cu_seqlens_q, slot_map, free_left, device_error, stream):
+    return load().inkling_rel_attn_build_tables(
+        _v(seq_lens), _v(new_lens), _v(page_table), page_table_stride, _v(free_pages),
+        _v(free_count), B, page_size, num_pages, max_tokens, _v(kv_lens), _v(cu_seqlens_q),
+        _v(slot_map), _v(free_left), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_kv_append_q4(k_new, v_new, slot_map, T, H_kv, D, page_size, num_pages, k_cache,
+                                  v_cache, device_error, stream):
+    return load().inkling_rel_attn_kv_append_q4(
+        _v(k_new), _v(v_new), _v(slot_map), T, H_kv, D, page_size, num_pages, _v(k_cache),
+        _v(v_cache), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_kv_read_q4(slot_map, k_cache, v_cache, T, H_kv, D, page_size, num_pages, k_rows,
+                                v_rows, device_error, stream):
+    return load().inkling_rel_attn_kv_read_q4(
+        _v(slot_map), _v(k_cache), _v(v_cache), T, H_kv, D, page_size, num_pages, _v(k_rows),
+        _v(v_rows), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_decode_q4(q, k_cache, v_cache, page_table, page_table_stride, seq_lens,
+                               rel_logits, B, q_len, H_q, H_kv, D, page_size, num_pages, R, window,
+                               scale, out, lse_out, workspace, workspace_bytes, device_error, stream):
+    return load().inkling_rel_attn_decode_q4(
+        _v(q), _v(k_cache), _v(v_cache), _v(page_table), page_table_stride, _v(seq_lens),
+        _v(rel_logits), B, q_len, H_q, H_kv, D, page_size, num_pages, R, window, scale, _v(out),
+        _v(lse_out), _v(workspace), workspace_bytes, _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_decode_q4_workspace_size(B, q_len, H_q, H_kv, D, num_sms):
+    return load().inkling_rel_attn_decode_q4_workspace_size(B, q_len, H_q, H_kv, D, num_sms)
+
+
+def inkling_rel_attn_prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, page_table_stride,
+                                seq_lens, rel_logits, B, T, max_q_len, H_q, H_kv, D, page_size,
+                                num_pages, R, window, scale, max_seq_len, out, lse_out, workspace,
+                                workspace_bytes, device_error, stream):
+    return load().inkling_rel_attn_prefill_q4(
+        _v(q), _v(cu_seqlens_q), _v(k_cache), _v(v_cache), _v(page_table), page_table_stride,
+        _v(seq_lens), _v(rel_logits), B, T, max_q_len, H_q, H_kv, D, page_size, num_pages, R,
+        window, scale, max_seq_len, _v(out), _v(lse_out), _v(workspace), workspace_bytes,
+        _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len):
+    return load().inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window,
+                                                             max_seq_len)
 
 
 def inkling_rel_attn_choose_splits(B, H_kv, window, max_seq_len, num_sms):

@@ -104,12 +104,7 @@ int sm_count() {
 }
 
 // ---------------------------------------------------------------- device info
-struct DevInfo {
-  int ok;  // 1 = sm_103, 0 = other, -1 = query failed
-  int sms;
-};
-
-static DevInfo device_info() {
+DevInfo device_info() {
   static std::atomic<int> cached_ok[kMaxDevices];
   static std::atomic<int> cached_sms[kMaxDevices];
   int dev = 0;
@@ -131,9 +126,9 @@ static DevInfo device_info() {
   return {ok, sms};
 }
 
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-static bool common_shape_ok(int32_t H_q, int32_t H_kv, int32_t D, int32_t P, int32_t num_pages,
+bool common_shape_ok(int32_t H_q, int32_t H_kv, int32_t D, int32_t P, int32_t num_pages,
                             int32_t R, int32_t pt_stride) {
   if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || H_q / H_kv > 16) return false;
   if (D != 64 && D != 128) return false;

@@ -25,6 +25,17 @@ bool smem_limit_on_device(const void* kern, int bytes, std::atomic<int>* done);
 // SMs of the current device (152 when the query fails).
 int sm_count();
 
+struct DevInfo {
+  int ok;  // 1 = sm_103, 0 = other, -1 = query failed
+  int sms;
+};
+DevInfo device_info();  // of the current device, cached
+
+// Checks shared by the entry points.
+bool aligned(const void* p, uintptr_t a);
+bool common_shape_ok(int32_t H_q, int32_t H_kv, int32_t D, int32_t P, int32_t num_pages, int32_t R,
+                     int32_t pt_stride);
+
 // Validated decode call, with the split plan resolved.
 struct DecodeCall {
   const void* q;
@@ -100,7 +111,76 @@ struct KvConvCall {
   cudaStream_t stream;
 };
 
+// Rows of the 4-bit cache by slot: appended (k_rows, v_rows read) or read back (written).
+struct Q4RowsCall {
+  void* k_rows;
+  void* v_rows;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slots;
+  int32_t T, H_kv, D, P, num_pages;
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
+// The visible part of a batch's sequences, expanded into bf16 pages of 64 tokens.
+struct Q4ExpandCall {
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  int32_t pt_stride;
+  const int32_t* cu_seqlens_q;
+  const int32_t* seq_lens;
+  int32_t B, H_kv, D, P, num_pages, window, pages_per_seq;
+  void* k_out;
+  void* v_out;
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
+struct DecodeQ4Call {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  int32_t pt_stride;
+  const int32_t* seq_lens;
+  const float* rel;
+  int32_t B, QL, H_q, H_kv, D, P, num_pages, R, window;
+  float scale;
+  void* out;
+  float* lse_out;
+  void* workspace;
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
+constexpr int32_t kTablesMaxBatch = 8192;  // requests of a build_tables call
+
+struct TablesCall {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* page_table;
+  int32_t pt_stride;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t B, P, num_pages, max_tokens;
+  int32_t* kv_lens;
+  int32_t* cu_seqlens_q;
+  int64_t* slot_map;
+  int32_t* free_left;
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
 int launch_decode(const DecodeCall& c);        // returns INKLING_* code
+int launch_q4_rows(const Q4RowsCall& c, bool append);
+int launch_q4_expand(const Q4ExpandCall& c);
+int launch_decode_q4(const DecodeQ4Call& c);
+int launch_build_tables(const TablesCall& c);
+size_t decode_q4_workspace_bytes(int32_t B, int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms);
 int launch_prefill(const PrefillCall& c);      // returns INKLING_* code
 int launch_kv_append(const KvAppendCall& c);   // returns INKLING_* code
 int launch_kv_conv_append(const KvConvCall& c);  // returns INKLING_* code

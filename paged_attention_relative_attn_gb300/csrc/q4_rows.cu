@@ -1,0 +1,247 @@
+// The 4-bit cache's rows: quantising append, read-back, and the expansion of
+// the visible part of a batch's sequences into bf16 pages for prefill.
+//
+// Operations: inkling_rel_attn_kv_append_q4, inkling_rel_attn_kv_read_q4 and
+// the first step of inkling_rel_attn_prefill_q4 in include/inkling_rel_attn.h.
+//
+// All three move rows and are bound by HBM.  A thread owns 8 adjacent channels
+// of K and the same 8 of V: 16 bytes each on the bf16 side, one 32-bit word
+// each on the 4-bit side; 4 adjacent lanes share a group and its scale, D / 8
+// lanes a row.  Reads and writes of a row's 4-bit side are D / 2 contiguous bytes.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "plan.cuh"
+#include "q4.cuh"
+
+namespace ira {
+
+constexpr int kRowThreads = 256;
+
+struct Q4RowsParams {
+  uint4* k_rows;  // [T][H_kv][D / 8] of 8 x bf16
+  uint4* v_rows;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  const int64_t* slots;
+  int32_t* dev_err;
+  int T, H_kv, P, num_pages;
+};
+
+// Word of a V row that this lane stores: lane i (group j = i / 4, t = i % 4)
+// holds the 16-bit units (g = 2t, j) and (2t + 1, j) of the row; a word has the
+// units (g, j) and (g, j + 1), j even.  The lanes of groups j and j + 1 swap
+// one unit each: the even one then has word (2t, j), the odd one (2t + 1, j - 1).
+template <int D>
+__device__ __forceinline__ int v_word(int j, int t) {
+  constexpr int N = D / kQ4Group;
+  return (N * (2 * t + (j & 1)) + (j & ~1)) >> 1;
+}
+__device__ __forceinline__ uint32_t v_swap(uint32_t units, int j) {
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, units, 4);
+  return (j & 1) ? __byte_perm(other, units, 0x7632) : __byte_perm(units, other, 0x5410);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    kv_append_q4_kernel(const __grid_constant__ Q4RowsParams p) {
+  constexpr int N = D / kQ4Group;
+  constexpr int U = D / 8;  // lanes per row
+  const int per_token = p.H_kv * U;
+  const size_t idx = (size_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const size_t total = (size_t)p.T * per_token;
+  const bool in = idx < total;  // total is a multiple of 8: lanes that exchange are in or out together
+  const int t_row = in ? (int)(idx / per_token) : 0;
+  const int u = (int)(idx - (size_t)t_row * per_token);
+  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
+  int64_t slot = -1;
+  if (in) {
+    kr = __ldcs(p.k_rows + idx);
+    vr = __ldcs(p.v_rows + idx);
+    slot = __ldg(p.slots + t_row);
+  }
+  const int h = u / U, i = u % U, j = i >> 2, t = i & 3;
+  uint32_t ks, vs;
+  const uint32_t kw = q4_quantise8(kr, ks);
+  const uint32_t vw = v_swap(q4_quantise8(vr, vs), j);
+  if (slot < 0) return;
+  if (slot >= (int64_t)p.num_pages * p.P) {
+    report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+    return;
+  }
+  const int page = (int)(slot / p.P), place = (int)(slot - (int64_t)page * p.P);
+  const size_t at = q4_block_at(page, h, place, p.H_kv, p.P, D);
+  const int r = place % kQ4Block;
+  uint8_t* kb = p.k_cache + at;
+  uint8_t* vb = p.v_cache + at;
+  reinterpret_cast<uint32_t*>(kb + r * (D / 2))[N * t + j] = kw;
+  reinterpret_cast<uint32_t*>(vb + r * (D / 2))[v_word<D>(j, t)] = vw;
+  if (t == 0) {
+    reinterpret_cast<uint16_t*>(kb + q4_scale_off(D))[r * N + j] = (uint16_t)ks;
+    reinterpret_cast<uint16_t*>(vb + q4_scale_off(D))[r * N + j] = (uint16_t)vs;
+  }
+}
+
+// The 8 K and 8 V channels (group j, quarter t) of row r of the blocks at kb, vb, as bf16.
+template <int D>
+__device__ __forceinline__ void q4_read8(const uint8_t* kb, const uint8_t* vb, int r, int j, int t,
+                                         uint4& k, uint4& v) {
+  constexpr int N = D / kQ4Group;
+  const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(kb + r * (D / 2)) + N * t + j);
+  const uint16_t* vrow = reinterpret_cast<const uint16_t*>(vb + r * (D / 2));
+  const uint32_t vw = (uint32_t)__ldg(vrow + N * (2 * t) + j) |
+                      ((uint32_t)__ldg(vrow + N * (2 * t + 1) + j) << 16);
+  const float ks = __uint_as_float(
+      (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(kb + q4_scale_off(D)) + r * N + j) << 16);
+  const float vs = __uint_as_float(
+      (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(vb + q4_scale_off(D)) + r * N + j) << 16);
+  k = make_uint4(q4_value2(kw, 0, ks), q4_value2(kw, 1, ks), q4_value2(kw, 2, ks), q4_value2(kw, 3, ks));
+  v = make_uint4(q4_value2(vw, 0, vs), q4_value2(vw, 1, vs), q4_value2(vw, 2, vs), q4_value2(vw, 3, vs));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    kv_read_q4_kernel(const __grid_constant__ Q4RowsParams p) {
+  constexpr int U = D / 8;
+  const int per_token = p.H_kv * U;
+  const size_t idx = (size_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (idx >= (size_t)p.T * per_token) return;
+  const int t_row = (int)(idx / per_token);
+  const int u = (int)(idx - (size_t)t_row * per_token);
+  const int64_t slot = __ldg(p.slots + t_row);
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  if (slot >= (int64_t)p.num_pages * p.P) {
+    report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+  } else if (slot >= 0) {
+    const int page = (int)(slot / p.P), place = (int)(slot - (int64_t)page * p.P);
+    const int h = u / U, i = u % U;
+    const size_t at = q4_block_at(page, h, place, p.H_kv, p.P, D);
+    q4_read8<D>(p.k_cache + at, p.v_cache + at, place % kQ4Block, i >> 2, i & 3, k, v);
+  }
+  p.k_rows[idx] = k;
+  p.v_rows[idx] = v;
+}
+
+static Q4RowsParams rows_params(const Q4RowsCall& c) {
+  Q4RowsParams p;
+  p.k_rows = static_cast<uint4*>(c.k_rows);
+  p.v_rows = static_cast<uint4*>(c.v_rows);
+  p.k_cache = static_cast<uint8_t*>(c.k_cache);
+  p.v_cache = static_cast<uint8_t*>(c.v_cache);
+  p.slots = c.slots;
+  p.dev_err = c.dev_err;
+  p.T = c.T;
+  p.H_kv = c.H_kv;
+  p.P = c.P;
+  p.num_pages = c.num_pages;
+  return p;
+}
+
+int launch_q4_rows(const Q4RowsCall& c, bool append) {
+  const Q4RowsParams p = rows_params(c);
+  const int64_t units = (int64_t)c.T * c.H_kv * (c.D / 8);
+  const int64_t blocks = (units + kRowThreads - 1) / kRowThreads;
+  if (blocks > INT32_MAX) return INKLING_ERR_ARG;
+  const unsigned g = (unsigned)blocks;
+  if (append) {
+    if (c.D == 128) kv_append_q4_kernel<128><<<g, kRowThreads, 0, c.stream>>>(p);
+    else kv_append_q4_kernel<64><<<g, kRowThreads, 0, c.stream>>>(p);
+  } else {
+    if (c.D == 128) kv_read_q4_kernel<128><<<g, kRowThreads, 0, c.stream>>>(p);
+    else kv_read_q4_kernel<64><<<g, kRowThreads, 0, c.stream>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Expansion for prefill: the keys that any query of sequence b's chunk sees,
+// [lo_b, L_b), go to bf16 pages of 64 tokens of the scratch pool, sequence b's
+// from page b * pages_per_seq on.  Its first key is base_b = lo_b rounded down
+// to 64, so the scratch sequence has length L_b - base_b; relative positions,
+// all that the attention uses, stay the same.  The scratch lengths and page
+// table are written for the attention that follows.  A sequence that the
+// scratch cannot hold, or whose chunk is longer than it is, gets length 0,
+// which the attention reports and skips.
+struct Q4ExpandParams {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* page_table;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  uint4* k_out;  // [B * pages_per_seq][64][H_kv][D / 8]
+  uint4* v_out;
+  int32_t* table_out;  // [B][pages_per_seq]
+  int32_t* lens_out;   // [B]
+  int32_t* dev_err;
+  int B, H_kv, P, num_pages, pt_stride, window, pages_per_seq;
+};
+
+constexpr int kExpandTokens = 16;  // tokens per block of the grid
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    q4_expand_kernel(const __grid_constant__ Q4ExpandParams p) {
+  constexpr int U = D / 8;
+  const int b = blockIdx.y;
+  const int q_len = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
+  const int L_in = __ldg(p.seq_lens + b);
+  const int L = min(max(L_in, 0), p.pt_stride * p.P);
+  const int lo = p.window > 0 ? max(0, L - q_len - p.window + 1) : 0;
+  const int base = lo & ~63;
+  const bool fits = q_len > 0 && q_len <= L && L - base <= p.pages_per_seq * 64;
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      p.lens_out[b] = fits ? L - base : 0;
+      if (L_in > L || (q_len > 0 && q_len <= L && !fits)) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
+    }
+    for (int i = threadIdx.x; i < p.pages_per_seq; i += kRowThreads)
+      p.table_out[(size_t)b * p.pages_per_seq + i] = b * p.pages_per_seq + i;
+  }
+  const int j0 = base + (int)blockIdx.x * kExpandTokens;  // all in one 16-token block of the cache
+  if (!fits || j0 >= L) return;
+  const int lp = j0 / p.P;
+  const int page = __ldg(p.page_table + (size_t)b * p.pt_stride + lp);
+  const bool ok = page >= 0 && page < p.num_pages;
+  if (!ok && threadIdx.x == 0) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+  const int n = min(kExpandTokens, L - j0) * p.H_kv * U;
+  const size_t dst0 = ((size_t)b * p.pages_per_seq * 64 + (j0 - base)) * p.H_kv * U;
+  for (int x = threadIdx.x; x < n; x += kRowThreads) {
+    const int r = x / (p.H_kv * U), u = x - r * (p.H_kv * U);
+    const int h = u / U, i = u % U;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (ok) {
+      const size_t at = q4_block_at(page, h, j0 - lp * p.P, p.H_kv, p.P, D);
+      q4_read8<D>(p.k_cache + at, p.v_cache + at, r, i >> 2, i & 3, k, v);
+    }
+    p.k_out[dst0 + x] = k;
+    p.v_out[dst0 + x] = v;
+  }
+}
+
+int launch_q4_expand(const Q4ExpandCall& c) {
+  Q4ExpandParams p;
+  p.k_cache = static_cast<const uint8_t*>(c.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(c.v_cache);
+  p.page_table = c.page_table;
+  p.cu = c.cu_seqlens_q;
+  p.seq_lens = c.seq_lens;
+  p.k_out = static_cast<uint4*>(c.k_out);
+  p.v_out = static_cast<uint4*>(c.v_out);
+  p.table_out = c.table_out;
+  p.lens_out = c.lens_out;
+  p.dev_err = c.dev_err;
+  p.B = c.B;
+  p.H_kv = c.H_kv;
+  p.P = c.P;
+  p.num_pages = c.num_pages;
+  p.pt_stride = c.pt_stride;
+  p.window = c.window;
+  p.pages_per_seq = c.pages_per_seq;
+  const dim3 grid((unsigned)(c.pages_per_seq * (64 / kExpandTokens)), (unsigned)c.B);
+  if (c.D == 128) q4_expand_kernel<128><<<grid, kRowThreads, 0, c.stream>>>(p);
+  else q4_expand_kernel<64><<<grid, kRowThreads, 0, c.stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA;
+}
+
+}  // namespace ira

@@ -248,6 +248,216 @@ def kv_conv_append(k_new, v_new, cu_seqlens_q, seq_lens, page_table, k_cache, v_
     _check(rc, "inkling_rel_attn_kv_conv_append")
 
 
+# ---------------------------------------------------------------------------
+# Step tables and the 4-bit cache
+# ---------------------------------------------------------------------------
+
+def _need_all(dev, specs):
+    """Type, rank, contiguity and device of a call's tensors: (tensor, name, dtype, dims); every
+    tensor is on ``dev``.  None is skipped (an optional argument not given)."""
+    for t, name, dtype, dims in specs:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.dim() != dims or t.device != dev or not t.is_contiguous():
+            _need(t, name, dtype, dims)
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
+
+
+def _launch(fn, where, dev, stream, *args):
+    """One call into the C ABI on ``dev`` (made current for it) and the given or current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: needs CUDA tensors, got {dev}")
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev, stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev, stream))
+    if rc != 0:
+        raise InklingError(rc, where)
+
+
+def _q4_cache(k_cache, v_cache):
+    """(num_pages, H_kv, page_size, D) of a pair of 4-bit pools."""
+    n, H_kv, P, row = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if row not in (36, 72):
+        raise ValueError(f"k_cache: rows of {row} bytes; 36 (D = 64) or 72 (D = 128) expected")
+    return n, H_kv, P, row * 16 // 9
+
+
+def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page_size, max_tokens=None,
+                 kv_lens=None, cu_seqlens_q=None, slot_map=None, free_left=None, device_error=None,
+                 stream=None):
+    """The tables of one serving step, from request lengths.  See
+    inkling_rel_attn_build_tables.
+
+    seq_lens, new_lens [B] int32 (new_lens < 0: the request has ended);
+    page_table [B, stride] int32, extended in place; free_pages [num_pages]
+    int32, a stack of free_count [1] int32 pages.  Returns (kv_lens [B] int32,
+    cu_seqlens_q [B + 1] int32, slot_map [max_tokens] int64, free_left [1] int32);
+    pass them to avoid allocations.  kv_lens=seq_lens and free_left=free_count
+    step the state in place.  max_tokens is slot_map's length when that is given.
+    """
+    dev = seq_lens.device
+    B = seq_lens.shape[0]
+    if kv_lens is None:
+        kv_lens = torch.empty_like(seq_lens)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slot_map is None:
+        if max_tokens is None:
+            raise ValueError("max_tokens or slot_map is needed")
+        slot_map = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    if free_left is None:
+        free_left = torch.empty_like(free_count)
+    _need_all(dev, ((seq_lens, "seq_lens", torch.int32, 1), (new_lens, "new_lens", torch.int32, 1),
+                    (page_table, "page_table", torch.int32, 2), (free_pages, "free_pages", torch.int32, 1),
+                    (free_count, "free_count", torch.int32, 1), (kv_lens, "kv_lens", torch.int32, 1),
+                    (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1), (slot_map, "slot_map", torch.int64, 1),
+                    (free_left, "free_left", torch.int32, 1), (device_error, "device_error", torch.int32, 1)))
+    if (new_lens.shape[0] != B or page_table.shape[0] != B or kv_lens.shape[0] != B
+            or cu_seqlens_q.shape[0] != B + 1 or free_count.shape[0] != 1 or free_left.shape[0] != 1
+            or max_tokens not in (None, slot_map.shape[0])):
+        raise ValueError("inconsistent shapes")
+    _launch(_lib.inkling_rel_attn_build_tables, "inkling_rel_attn_build_tables", dev, stream,
+            seq_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+            free_pages.data_ptr(), free_count.data_ptr(), B, page_size, free_pages.shape[0],
+            slot_map.shape[0], kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), slot_map.data_ptr(),
+            free_left.data_ptr(), _ptr(device_error))
+    return kv_lens, cu_seqlens_q, slot_map, free_left
+
+
+def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None, stream=None):
+    """Quantise the new tokens' K/V rows into the 4-bit paged cache (in place).
+    See inkling_rel_attn_kv_append_q4.
+
+    k_new, v_new [T, H_kv, D] bf16; slot_map [T] int64 (page * page_size + place,
+    negative: skipped); k_cache, v_cache [num_pages, H_kv, page_size, 9 * D / 16]
+    uint8.
+    """
+    dev = k_new.device
+    _need_all(dev, ((k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
+                    (slot_map, "slot_map", torch.int64, 1), (k_cache, "k_cache", torch.uint8, 4),
+                    (v_cache, "v_cache", torch.uint8, 4), (device_error, "device_error", torch.int32, 1)))
+    T, H_kv, D = k_new.shape
+    n, H, P, D_c = _q4_cache(k_cache, v_cache)
+    if v_new.shape != k_new.shape or (H, D_c) != (H_kv, D) or slot_map.shape[0] != T:
+        raise ValueError("inconsistent shapes")
+    _launch(_lib.inkling_rel_attn_kv_append_q4, "inkling_rel_attn_kv_append_q4", dev, stream,
+            k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), T, H_kv, D, P, n,
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(device_error))
+
+
+def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_error=None, stream=None):
+    """Rows of the 4-bit cache as the bf16 values they stand for.  See
+    inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
+    """
+    dev = k_cache.device
+    _need_all(dev, ((k_cache, "k_cache", torch.uint8, 4), (v_cache, "v_cache", torch.uint8, 4)))
+    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    T = slot_map.shape[0]
+    if k_rows is None:
+        k_rows = torch.empty((T, H_kv, D), dtype=torch.bfloat16, device=dev)
+    if v_rows is None:
+        v_rows = torch.empty((T, H_kv, D), dtype=torch.bfloat16, device=dev)
+    _need_all(dev, ((slot_map, "slot_map", torch.int64, 1), (k_rows, "k_rows", torch.bfloat16, 3),
+                    (v_rows, "v_rows", torch.bfloat16, 3), (device_error, "device_error", torch.int32, 1)))
+    if k_rows.shape != (T, H_kv, D) or v_rows.shape != (T, H_kv, D):
+        raise ValueError("inconsistent shapes")
+    _launch(_lib.inkling_rel_attn_kv_read_q4, "inkling_rel_attn_kv_read_q4", dev, stream,
+            slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H_kv, D, P, n,
+            k_rows.data_ptr(), v_rows.data_ptr(), _ptr(device_error))
+    return k_rows, v_rows
+
+
+def decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D, num_sms=0):
+    return _lib.inkling_rel_attn_decode_q4_workspace_size(B, q_len, H_q, H_kv, D, num_sms)
+
+
+def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1, window, scale, out=None,
+              lse=None, workspace=None, device_error=None, stream=None):
+    """Decode of the last ``q_len`` tokens of each sequence over the 4-bit cache.
+    See inkling_rel_attn_decode_q4.
+
+    q [B * q_len, H_q, D] bf16 (row b * q_len + i); k_cache, v_cache [num_pages,
+    H_kv, page_size, 9 * D / 16] uint8; page_table [B, stride] int32; seq_lens
+    [B] int32; rel_logits [B * q_len, H_q, R] fp32.  Returns (out bf16 like q,
+    lse fp32 [B * q_len, H_q]).  Pass ``out``, ``lse`` and ``workspace``
+    (decode_q4_workspace_bytes) to avoid allocations.
+    """
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    _need_all(dev, ((q, "q", torch.bfloat16, 3), (k_cache, "k_cache", torch.uint8, 4),
+                    (v_cache, "v_cache", torch.uint8, 4), (page_table, "page_table", torch.int32, 2),
+                    (seq_lens, "seq_lens", torch.int32, 1), (rel_logits, "rel_logits", torch.float32, 3),
+                    (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2),
+                    (device_error, "device_error", torch.int32, 1)))
+    T, H_q, D = q.shape
+    B = seq_lens.shape[0]
+    n, H_kv, P, D_c = _q4_cache(k_cache, v_cache)
+    if (D_c != D or T != B * q_len or rel_logits.shape[:2] != (T, H_q) or page_table.shape[0] != B
+            or out.shape != q.shape or lse.shape != (T, H_q)):
+        raise ValueError("inconsistent shapes")
+    if workspace is None:
+        workspace = torch.empty(decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the device of q")
+    _launch(_lib.inkling_rel_attn_decode_q4, "inkling_rel_attn_decode_q4", dev, stream,
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+            seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, rel_logits.shape[2],
+            window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(device_error))
+    return out, lse
+
+
+def prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len):
+    return _lib.inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len)
+
+
+def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, window, scale,
+               max_seq_len, max_q_len, out=None, lse=None, workspace=None, device_error=None, stream=None):
+    """Chunked / paged prefill over the 4-bit cache.  See inkling_rel_attn_prefill_q4.
+
+    q [T, H_q, D] bf16; cu_seqlens_q [B + 1] int32; rel_logits [T, H_q, R] fp32;
+    the cache, page_table and seq_lens as for ``decode_q4``; max_seq_len and
+    max_q_len are host bounds.  Returns (out bf16 [T, H_q, D], lse fp32 [T, H_q]).
+    Pass ``out``, ``lse`` and ``workspace`` (prefill_q4_workspace_bytes) to avoid
+    allocations.
+    """
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    _need_all(dev, ((q, "q", torch.bfloat16, 3), (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1),
+                    (k_cache, "k_cache", torch.uint8, 4), (v_cache, "v_cache", torch.uint8, 4),
+                    (page_table, "page_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
+                    (rel_logits, "rel_logits", torch.float32, 3), (out, "out", torch.bfloat16, 3),
+                    (lse, "lse", torch.float32, 2), (device_error, "device_error", torch.int32, 1)))
+    T, H_q, D = q.shape
+    B = seq_lens.shape[0]
+    n, H_kv, P, D_c = _q4_cache(k_cache, v_cache)
+    if (D_c != D or cu_seqlens_q.shape[0] != B + 1 or rel_logits.shape[:2] != (T, H_q)
+            or page_table.shape[0] != B or out.shape != q.shape or lse.shape != (T, H_q)):
+        raise ValueError("inconsistent shapes")
+    if workspace is None:
+        workspace = torch.empty(prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len),
+                                dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the device of q")
+    _launch(_lib.inkling_rel_attn_prefill_q4, "inkling_rel_attn_prefill_q4", dev, stream,
+            q.data_ptr(), cu_seqlens_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
+            max_q_len, H_q, H_kv, D, P, n, rel_logits.shape[2], window, scale, max_seq_len, out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _ptr(device_error))
+    return out, lse
+
+
 def decode_inputs(inp, **kw):
     """``decode`` on a workloads.DecodeInputs-like object."""
     return decode(inp.q, inp.k_cache, inp.v_cache, inp.page_table, inp.seq_lens, inp.rel_logits,
