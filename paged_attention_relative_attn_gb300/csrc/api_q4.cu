@@ -172,6 +172,7 @@ int inkling_rel_attn_decode_q4(const void* q, const void* k_cache, const void* v
   c.out = out;
   c.lse_out = lse_out;
   c.workspace = workspace;
+  c.sms = di.sms;
   c.dev_err = device_error;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_decode_q4(c);

@@ -153,6 +153,7 @@ struct DecodeQ4Call {
   void* out;
   float* lse_out;
   void* workspace;
+  int32_t sms;  // of the device
   int32_t* dev_err;
   cudaStream_t stream;
 };
