@@ -23,9 +23,9 @@
 // mma.sync m16n8k16 in bf16 (rows are the N side, so 3 or 6 heads waste no M):
 //  * a nibble u becomes the bf16 number 128 + u by or-ing it into the mantissa
 //    of 128 -- one instruction for two values; the excess 136 over x = u - 8 is
-//    taken out by products with a constant matrix of -136: once per item for K
-//    (the accumulators of a group start at -136 sum(q)), and with the same
-//    rounded P for V, block by block, so that no large sums cancel later;
+//    taken out by products: of the scales and -136 sum(q) for K (one more product
+//    for all groups), and of a constant -136 and the same rounded P for V, block by
+//    block, so that no large sums cancel later;
 //  * a group's scale is a factor of its own accumulator for K, in fp32, and of
 //    P for V, before P is rounded to bf16 (the operand type of the product; 2^-8
 //    of a weight at most, as the bf16 cache's decode rounds it).
@@ -98,21 +98,23 @@ struct Dq4Smem {
   }
 };
 
-// Nibble n (0..3) of both halves of w as the bf16 pair 128 + u.
+// Nibble n (0..3) of both halves of w as the bf16 pair 128 + u: (w >> 4n & mask) | 128, one lop3.
 template <int n>
 __device__ __forceinline__ uint32_t q4_expand(uint32_t w) {
-  return ((w >> (4 * n)) & 0x000f000fu) | 0x43004300u;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * n)), "r"(0x000f000fu), "r"(0x43004300u));
+  return r;
 }
 constexpr uint32_t kMinus136 = 0xc308c308u;
 
-// mma_16816 into a new accumulator that starts at c0 (even columns) and c1 (odd ones).
-__device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1, float c0, float c1) {
+// mma_16816 into a new accumulator.
+__device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%10,%11};"
+      "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Positions and blocks of token group `grp` of a sequence of length L >= QL.
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
             }
           }
           if (__all_sync(0xffffffffu, !todo)) break;
+          __nanosleep(100);  // about the time of two blocks at full bandwidth; the ring holds tens
           if ((tries & 31u) == 0) {  // bounded, as mbar_wait
             if (t0 == 0) t0 = globaltimer();
             if (__any_sync(0xffffffffu, *abort_flag || globaltimer() - t0 > kWaitTimeoutNs)) {
@@ -411,13 +414,15 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
     const Dq4Item it = *item_rec(is);
     if (it.nblk == 0) break;
     const int rows = it.tn * G;
-    // ---- q fragments (channel order of the K rows) and -136 sum(q) per group
+    // ---- q fragments (channel order of the K rows), and -136 sum(q) of every group
+    // as an operand of one more product, with the block's scales: sum_j s_j (-136 sum_j(q))
     uint32_t qf[N][2][NT][2];
-    float qsum[N][NT][2];
+    uint32_t qs[NT][2];  // B fragment of -136 sum(q): k = N * part + group, three bf16 parts
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
       const uint8_t* qr = item_q(is) + r * D * 2;
+      float sum[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         uint4 w = make_uint4(0, 0, 0, 0);  // channels 32j + 8t + 0..7
@@ -426,13 +431,25 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
         qf[j][0][nt][1] = __byte_perm(w.x, w.z, 0x7632);
         qf[j][1][nt][0] = __byte_perm(w.y, w.w, 0x5410);
         qf[j][1][nt][1] = __byte_perm(w.y, w.w, 0x7632);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          mma_16816(c, kMinus136, kMinus136, kMinus136, kMinus136, qf[j][i][nt][0], qf[j][i][nt][1]);
-        qsum[j][nt][0] = c[0];
-        qsum[j][nt][1] = c[1];
+        float c[4];
+        mma_16816_new(c, kMinus136, kMinus136, kMinus136, kMinus136, qf[j][0][nt][0], qf[j][0][nt][1]);
+        mma_16816(c, kMinus136, kMinus136, kMinus136, kMinus136, qf[j][1][nt][0], qf[j][1][nt][1]);
+        // every row of c is the same; this lane takes column g
+        const float even = __shfl_sync(0xffffffffu, c[0], g >> 1), odd = __shfl_sync(0xffffffffu, c[1], g >> 1);
+        sum[j] = (g & 1) ? odd : even;
       }
+      // k = 2t, 2t + 1 and 2t + 8, 2t + 9 of column g
+      auto part = [&](float v, int i) {  // part i of v's three bf16 parts
+        float h = __bfloat162float(__float2bfloat16(v));
+        if (i == 0) return h;
+        v -= h;
+        h = __bfloat162float(__float2bfloat16(v));
+        return i == 1 ? h : v - h;
+      };
+      const float lo_ = N == 2 || !(t & 1) ? sum[0] : sum[N - 2], hi_ = N == 2 || !(t & 1) ? sum[1] : sum[N - 1];
+      const int p0 = N == 2 ? t : t >> 1;  // of k = 2t; k = 2t + 8 is two further on
+      qs[nt][0] = p0 < 3 ? pack_bf16(part(lo_, p0), part(hi_, p0)) : 0u;
+      qs[nt][1] = N == 4 && t < 2 ? pack_bf16(part(lo_, 2), part(hi_, 2)) : 0u;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(rempty + is));
@@ -449,8 +466,20 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
         const int r = min(nt * 8 + 2 * t + x, rows - 1), i = r / G;
         bias_at[nt][x] = p.rel + ((size_t)it.row0 + (size_t)i * p.H_q + (r - i * G)) * p.R + (pos0 + i - key_g);
       }
+    float far[NT][2];  // bias at and past the table's end
+    const bool has_far = pos1 - it.blk0 * 16 >= p.R;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        far[nt][x] = has_far ? __ldg(bias_at[nt][x] - (pos0 + row_tok(nt, x) - key_g) + p.R - 1) : 0.f;
     auto load_bias = [&](int key0, float (&bv)[NT][4]) {
-      if (key0 + 15 <= pos0 && pos1 - key0 < p.R) {  // every distance is inside the table
+      if (pos0 - (key0 + 15) >= p.R - 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) bv[nt][x] = far[nt][x & 1];
+      } else if (key0 + 15 <= pos0 && pos1 - key0 < p.R) {  // every distance is inside the table
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,12 +551,14 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
         return __uint_as_float((j & 1) ? sc[x][j >> 1] & 0xffff0000u : sc[x][j >> 1] << 16);
       };
 
-      // ---- scores of 16 keys x rows
+      // ---- scores of 16 keys x rows, from sum_j s_j (-136 sum_j(q)) on
       float sc[NT][4];
+      {
+        const int w = N == 4 ? t & 1 : 0;  // scales of groups 2w, 2w + 1 against k = 2t, 2t + 1 (and + 8)
+        const uint32_t a0 = w ? ksc[0][N / 2 - 1] : ksc[0][0], a1 = w ? ksc[1][N / 2 - 1] : ksc[1][0];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nt][x] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) mma_16816_new(sc[nt], a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
+      }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const uint32_t a0 = q4_expand<0>(kw[0][j]), a1 = q4_expand<0>(kw[1][j]), a2 = q4_expand<1>(kw[0][j]),
@@ -538,7 +569,7 @@ __global__ void __launch_bounds__(Dq4Shape<NT>::kThreads, Dq4Shape<NT>::kCtas)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float c[4];
-          mma_16816_c(c, a0, a1, a2, a3, qf[j][0][nt][0], qf[j][0][nt][1], qsum[j][nt][0], qsum[j][nt][1]);
+          mma_16816_new(c, a0, a1, a2, a3, qf[j][0][nt][0], qf[j][0][nt][1]);
           mma_16816(c, b0, b1, b2, b3, qf[j][1][nt][0], qf[j][1][nt][1]);
           sc[nt][0] = fmaf(c[0], s0, sc[nt][0]);
           sc[nt][1] = fmaf(c[1], s0, sc[nt][1]);
