@@ -82,29 +82,27 @@ def reference(inp, q=None, rel=None):
 
 
 def score_error(inp):
-    """Bound on the absolute error of a score [T, H_q, 1].  A score is a sum of D products q x s in fp32, formed
-    as q (128 + u) s less 136 q s: terms of magnitude up to 151 |q| s, each addition off by at most 2^-23 of
-    the largest partial sum (the matrix unit cuts rather than rounds), 4 additions of 16-term sums per
-    group.  4 * 2^-23 * 151 * sum|q| * s < 2^-14 sum|q| s would be the worst case with every term of one sign;
-    the largest partial sum is then sum|q| * 151 s, so this is that bound."""
-    return 4 * 2.0 ** -23 * 151 * S_MAX * inp.scale * np.abs(f64(inp.q)).sum(-1, keepdims=True)
+    """Bound on the absolute error of a score [T, H_q, 1].
+    fp32: a score is a sum of products q u s less 8 q s, terms of magnitude up to 23 |q| s, each addition off by at
+    most 2^-23 of the largest partial sum (the matrix unit cuts rather than rounds), 4 additions of 32-term sums
+    per group: 4 * 2^-23 * 23 * S_MAX * sum|q|."""
+    return 4 * 2.0 ** -23 * 23 * S_MAX * abs(inp.scale) * np.abs(f64(inp.q)).sum(-1, keepdims=True)
 
 
 def check(inp, out, lse, ref=None, what=""):
     """bf16 outputs: P is rounded to bf16 (2^-8 of every weight) and the result again (2^-8), and a score error
     e changes a weight by a factor within 1 + 2e (its own and the sum's); hardware exponentials and fp32 sums are
     worth 2^-20.  The logarithm of the sum moves by e; fp32 holds it to 2^-22 of itself.
-    The products with V are P s (128 + u) less 136 P s, so a key whose value is 0 still brings fp32 rounding: two
-    additions for each of the two products of a 16-key block, each cut at 2^-23 of a partial sum of at most
-    151 s P beside what is there already: 4 * 2^-23 * 151 * s_max for all keys (P sums to 1), and 2^-23 of the sum so
-    far, at most ``size``, for each of 4 additions per block."""
+    The products with V are P s u less 8 P s, summed apart: partial sums of at most 15 S_MAX and 8 S_MAX (P sums to
+    1), each addition cut at 2^-23 of one, two per 16-key block; and 2^-23 of the sum so far, at most ``size``, for
+    each of as many additions."""
     ro, rl, size = reference(inp) if ref is None else ref
     e = score_error(inp)
     g, gl = f64(out), f64(lse)
     assert np.isfinite(g).all(), f"{what}: non-finite output"
     blocks = inp.max_seq_len / 16 + 2
     tol = 2.0 ** -8 * (np.abs(ro) + size) * (1 + 2.0 ** -7) + (2 * e + 2.0 ** -20) * size
-    tol += 4 * 2.0 ** -23 * (151 * S_MAX + blocks * size)
+    tol += 2 * blocks * 2.0 ** -23 * (23 * S_MAX + size)
     bad = np.abs(g - ro) > tol
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {(np.abs(g - ro) / tol).max():.2f} of the bound"
     fin = np.isfinite(rl)
