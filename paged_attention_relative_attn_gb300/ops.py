@@ -252,37 +252,70 @@ def kv_conv_append(k_new, v_new, cu_seqlens_q, seq_lens, page_table, k_cache, v_
 # Step tables and the 4-bit cache
 # ---------------------------------------------------------------------------
 
-def _need_all(dev, specs):
-    """Type, rank, contiguity and device of a call's tensors: (tensor, name, dtype, dims); every
-    tensor is on ``dev``.  None is skipped (an optional argument not given)."""
+# A decode step calls several of these with a few microseconds of GPU work each, so their
+# checks are one expression per call; what fails it is named by _refuse.
+
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+def _refuse(dev, specs):
+    """Raise for the first (tensor, name, dtype, dims) that is not a contiguous tensor of that type and rank
+    on device ``dev``; shapes that do not go together if each is."""
     for t, name, dtype, dims in specs:
-        if t is None:
-            continue
-        if t.dtype is not dtype or t.dim() != dims or t.device != dev or not t.is_contiguous():
-            _need(t, name, dtype, dims)
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.dim() != dims:
+            raise ValueError(f"{name}: expected {dims} dims, got shape {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, not on the other tensors' device")
+    raise ValueError("inconsistent shapes")
 
 
-def _launch(fn, where, dev, stream, *args):
-    """One call into the C ABI on ``dev`` (made current for it) and the given or current stream."""
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: needs CUDA tensors, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(dev, stream))
+def _launch(name, dev, stream, *args):
+    """One call into the C ABI on device ``dev`` (made current for it) and the given or current stream."""
+    if dev < 0:
+        raise ValueError(f"{name}: needs CUDA tensors")
+    fn = getattr(_lib.load(), name)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev, stream))
+            rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
-        raise InklingError(rc, where)
+        raise InklingError(rc, name)
+
+
+def _error_word(device_error, dev):
+    """Address of the optional error word."""
+    if device_error is None:
+        return None
+    if device_error.dtype is not _I32 or device_error.get_device() != dev or device_error.dim() != 1:
+        raise TypeError("device_error: expected one int32 on the other tensors' device")
+    return device_error.data_ptr()
+
+
+def _workspace(workspace, need, q):
+    """(workspace, bytes): the given one, or a new one of ``need()`` bytes."""
+    if workspace is None:
+        workspace = torch.empty(need(), dtype=_U8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the device of q")
+    return workspace, workspace.nbytes
 
 
 def _q4_cache(k_cache, v_cache):
-    """(num_pages, H_kv, page_size, D) of a pair of 4-bit pools."""
+    """(num_pages, H_kv, page_size, D) of a pair of 4-bit pools; their devices are the caller's check."""
+    if k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or k_cache.dim() != 4:
+        raise TypeError("k_cache, v_cache: uint8 pools [num_pages, H_kv, page_size, 9 * D / 16] expected")
     n, H_kv, P, row = k_cache.shape
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
     if row not in (36, 72):
         raise ValueError(f"k_cache: rows of {row} bytes; 36 (D = 64) or 72 (D = 128) expected")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache, v_cache: must be contiguous")
     return n, H_kv, P, row * 16 // 9
 
 
@@ -299,32 +332,39 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     pass them to avoid allocations.  kv_lens=seq_lens and free_left=free_count
     step the state in place.  max_tokens is slot_map's length when that is given.
     """
-    dev = seq_lens.device
     B = seq_lens.shape[0]
     if kv_lens is None:
         kv_lens = torch.empty_like(seq_lens)
     if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        cu_seqlens_q = torch.empty(B + 1, dtype=_I32, device=seq_lens.device)
     if slot_map is None:
         if max_tokens is None:
             raise ValueError("max_tokens or slot_map is needed")
-        slot_map = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        slot_map = torch.empty(max_tokens, dtype=_I64, device=seq_lens.device)
     if free_left is None:
         free_left = torch.empty_like(free_count)
-    _need_all(dev, ((seq_lens, "seq_lens", torch.int32, 1), (new_lens, "new_lens", torch.int32, 1),
-                    (page_table, "page_table", torch.int32, 2), (free_pages, "free_pages", torch.int32, 1),
-                    (free_count, "free_count", torch.int32, 1), (kv_lens, "kv_lens", torch.int32, 1),
-                    (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1), (slot_map, "slot_map", torch.int64, 1),
-                    (free_left, "free_left", torch.int32, 1), (device_error, "device_error", torch.int32, 1)))
-    if (new_lens.shape[0] != B or page_table.shape[0] != B or kv_lens.shape[0] != B
-            or cu_seqlens_q.shape[0] != B + 1 or free_count.shape[0] != 1 or free_left.shape[0] != 1
-            or max_tokens not in (None, slot_map.shape[0])):
-        raise ValueError("inconsistent shapes")
-    _launch(_lib.inkling_rel_attn_build_tables, "inkling_rel_attn_build_tables", dev, stream,
+    dev = seq_lens.get_device()
+    if not (seq_lens.dtype is new_lens.dtype is page_table.dtype is free_pages.dtype is free_count.dtype
+            is kv_lens.dtype is cu_seqlens_q.dtype is free_left.dtype is _I32 and slot_map.dtype is _I64
+            and new_lens.get_device() == page_table.get_device() == free_pages.get_device()
+            == free_count.get_device() == kv_lens.get_device() == cu_seqlens_q.get_device()
+            == slot_map.get_device() == free_left.get_device() == dev
+            and seq_lens.is_contiguous() and new_lens.is_contiguous() and page_table.is_contiguous()
+            and free_pages.is_contiguous() and kv_lens.is_contiguous() and cu_seqlens_q.is_contiguous()
+            and slot_map.is_contiguous() and seq_lens.dim() == 1 and new_lens.shape == kv_lens.shape == seq_lens.shape
+            and page_table.dim() == 2 and page_table.shape[0] == B and cu_seqlens_q.shape == (B + 1,)
+            and free_pages.dim() == slot_map.dim() == 1 and free_count.shape == free_left.shape == (1,)
+            and max_tokens in (None, slot_map.shape[0])):
+        _refuse(dev, ((seq_lens, "seq_lens", _I32, 1), (new_lens, "new_lens", _I32, 1),
+                      (page_table, "page_table", _I32, 2), (free_pages, "free_pages", _I32, 1),
+                      (free_count, "free_count", _I32, 1), (kv_lens, "kv_lens", _I32, 1),
+                      (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (slot_map, "slot_map", _I64, 1),
+                      (free_left, "free_left", _I32, 1)))
+    _launch("inkling_rel_attn_build_tables", dev, stream,
             seq_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             free_pages.data_ptr(), free_count.data_ptr(), B, page_size, free_pages.shape[0],
             slot_map.shape[0], kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), slot_map.data_ptr(),
-            free_left.data_ptr(), _ptr(device_error))
+            free_left.data_ptr(), _error_word(device_error, dev))
     return kv_lens, cu_seqlens_q, slot_map, free_left
 
 
@@ -336,38 +376,40 @@ def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None,
     negative: skipped); k_cache, v_cache [num_pages, H_kv, page_size, 9 * D / 16]
     uint8.
     """
-    dev = k_new.device
-    _need_all(dev, ((k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
-                    (slot_map, "slot_map", torch.int64, 1), (k_cache, "k_cache", torch.uint8, 4),
-                    (v_cache, "v_cache", torch.uint8, 4), (device_error, "device_error", torch.int32, 1)))
-    T, H_kv, D = k_new.shape
-    n, H, P, D_c = _q4_cache(k_cache, v_cache)
-    if v_new.shape != k_new.shape or (H, D_c) != (H_kv, D) or slot_map.shape[0] != T:
-        raise ValueError("inconsistent shapes")
-    _launch(_lib.inkling_rel_attn_kv_append_q4, "inkling_rel_attn_kv_append_q4", dev, stream,
+    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    T = slot_map.shape[0]
+    dev = k_new.get_device()
+    if not (k_new.dtype is v_new.dtype is _BF16 and slot_map.dtype is _I64
+            and v_new.get_device() == slot_map.get_device() == k_cache.get_device() == v_cache.get_device() == dev
+            and k_new.is_contiguous() and v_new.is_contiguous() and slot_map.is_contiguous()
+            and k_new.shape == v_new.shape == (T, H_kv, D) and slot_map.dim() == 1):
+        _refuse(dev, ((k_new, "k_new", _BF16, 3), (v_new, "v_new", _BF16, 3), (slot_map, "slot_map", _I64, 1),
+                      (k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4)))
+    _launch("inkling_rel_attn_kv_append_q4", dev, stream,
             k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), T, H_kv, D, P, n,
-            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(device_error))
+            k_cache.data_ptr(), v_cache.data_ptr(), _error_word(device_error, dev))
 
 
 def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_error=None, stream=None):
     """Rows of the 4-bit cache as the bf16 values they stand for.  See
     inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
     """
-    dev = k_cache.device
-    _need_all(dev, ((k_cache, "k_cache", torch.uint8, 4), (v_cache, "v_cache", torch.uint8, 4)))
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
     T = slot_map.shape[0]
     if k_rows is None:
-        k_rows = torch.empty((T, H_kv, D), dtype=torch.bfloat16, device=dev)
+        k_rows = torch.empty((T, H_kv, D), dtype=_BF16, device=k_cache.device)
     if v_rows is None:
-        v_rows = torch.empty((T, H_kv, D), dtype=torch.bfloat16, device=dev)
-    _need_all(dev, ((slot_map, "slot_map", torch.int64, 1), (k_rows, "k_rows", torch.bfloat16, 3),
-                    (v_rows, "v_rows", torch.bfloat16, 3), (device_error, "device_error", torch.int32, 1)))
-    if k_rows.shape != (T, H_kv, D) or v_rows.shape != (T, H_kv, D):
-        raise ValueError("inconsistent shapes")
-    _launch(_lib.inkling_rel_attn_kv_read_q4, "inkling_rel_attn_kv_read_q4", dev, stream,
+        v_rows = torch.empty((T, H_kv, D), dtype=_BF16, device=k_cache.device)
+    dev = k_cache.get_device()
+    if not (k_rows.dtype is v_rows.dtype is _BF16 and slot_map.dtype is _I64
+            and v_cache.get_device() == slot_map.get_device() == k_rows.get_device() == v_rows.get_device() == dev
+            and k_rows.is_contiguous() and v_rows.is_contiguous() and slot_map.is_contiguous()
+            and k_rows.shape == v_rows.shape == (T, H_kv, D) and slot_map.dim() == 1):
+        _refuse(dev, ((k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4), (slot_map, "slot_map", _I64, 1),
+                      (k_rows, "k_rows", _BF16, 3), (v_rows, "v_rows", _BF16, 3)))
+    _launch("inkling_rel_attn_kv_read_q4", dev, stream,
             slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H_kv, D, P, n,
-            k_rows.data_ptr(), v_rows.data_ptr(), _ptr(device_error))
+            k_rows.data_ptr(), v_rows.data_ptr(), _error_word(device_error, dev))
     return k_rows, v_rows
 
 
@@ -386,31 +428,32 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
     lse fp32 [B * q_len, H_q]).  Pass ``out``, ``lse`` and ``workspace``
     (decode_q4_workspace_bytes) to avoid allocations.
     """
-    dev = q.device
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    _need_all(dev, ((q, "q", torch.bfloat16, 3), (k_cache, "k_cache", torch.uint8, 4),
-                    (v_cache, "v_cache", torch.uint8, 4), (page_table, "page_table", torch.int32, 2),
-                    (seq_lens, "seq_lens", torch.int32, 1), (rel_logits, "rel_logits", torch.float32, 3),
-                    (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2),
-                    (device_error, "device_error", torch.int32, 1)))
-    T, H_q, D = q.shape
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    T, H_q = q.shape[:2]
     B = seq_lens.shape[0]
-    n, H_kv, P, D_c = _q4_cache(k_cache, v_cache)
-    if (D_c != D or T != B * q_len or rel_logits.shape[:2] != (T, H_q) or page_table.shape[0] != B
-            or out.shape != q.shape or lse.shape != (T, H_q)):
-        raise ValueError("inconsistent shapes")
-    if workspace is None:
-        workspace = torch.empty(decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous and on the device of q")
-    _launch(_lib.inkling_rel_attn_decode_q4, "inkling_rel_attn_decode_q4", dev, stream,
+    dev = q.get_device()
+    if not (q.dtype is out.dtype is _BF16 and page_table.dtype is seq_lens.dtype is _I32
+            and rel_logits.dtype is lse.dtype is _F32
+            and k_cache.get_device() == v_cache.get_device() == page_table.get_device() == seq_lens.get_device()
+            == rel_logits.get_device() == out.get_device() == lse.get_device() == dev
+            and q.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
+            and rel_logits.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
+            and q.shape == out.shape == (B * q_len, H_q, D) and lse.shape == (T, H_q) and seq_lens.dim() == 1
+            and rel_logits.dim() == 3 and rel_logits.shape[:2] == (T, H_q)
+            and page_table.dim() == 2 and page_table.shape[0] == B):
+        _refuse(dev, ((q, "q", _BF16, 3), (k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4),
+                      (page_table, "page_table", _I32, 2), (seq_lens, "seq_lens", _I32, 1),
+                      (rel_logits, "rel_logits", _F32, 3), (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
+    workspace, ws_bytes = _workspace(workspace, lambda: decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), q)
+    _launch("inkling_rel_attn_decode_q4", dev, stream,
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, rel_logits.shape[2],
-            window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _ptr(device_error))
+            window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
+            _error_word(device_error, dev))
     return out, lse
 
 
@@ -428,33 +471,35 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
     Pass ``out``, ``lse`` and ``workspace`` (prefill_q4_workspace_bytes) to avoid
     allocations.
     """
-    dev = q.device
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    _need_all(dev, ((q, "q", torch.bfloat16, 3), (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1),
-                    (k_cache, "k_cache", torch.uint8, 4), (v_cache, "v_cache", torch.uint8, 4),
-                    (page_table, "page_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
-                    (rel_logits, "rel_logits", torch.float32, 3), (out, "out", torch.bfloat16, 3),
-                    (lse, "lse", torch.float32, 2), (device_error, "device_error", torch.int32, 1)))
-    T, H_q, D = q.shape
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    T, H_q = q.shape[:2]
     B = seq_lens.shape[0]
-    n, H_kv, P, D_c = _q4_cache(k_cache, v_cache)
-    if (D_c != D or cu_seqlens_q.shape[0] != B + 1 or rel_logits.shape[:2] != (T, H_q)
-            or page_table.shape[0] != B or out.shape != q.shape or lse.shape != (T, H_q)):
-        raise ValueError("inconsistent shapes")
-    if workspace is None:
-        workspace = torch.empty(prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len),
-                                dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous and on the device of q")
-    _launch(_lib.inkling_rel_attn_prefill_q4, "inkling_rel_attn_prefill_q4", dev, stream,
+    dev = q.get_device()
+    if not (q.dtype is out.dtype is _BF16
+            and page_table.dtype is seq_lens.dtype is cu_seqlens_q.dtype is _I32
+            and rel_logits.dtype is lse.dtype is _F32
+            and k_cache.get_device() == v_cache.get_device() == page_table.get_device() == seq_lens.get_device()
+            == cu_seqlens_q.get_device() == rel_logits.get_device() == out.get_device() == lse.get_device() == dev
+            and q.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
+            and cu_seqlens_q.is_contiguous() and rel_logits.is_contiguous() and out.is_contiguous()
+            and lse.is_contiguous() and q.shape == out.shape == (T, H_q, D) and lse.shape == (T, H_q)
+            and seq_lens.dim() == 1 and cu_seqlens_q.shape == (B + 1,) and rel_logits.dim() == 3
+            and rel_logits.shape[:2] == (T, H_q) and page_table.dim() == 2 and page_table.shape[0] == B):
+        _refuse(dev, ((q, "q", _BF16, 3), (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (k_cache, "k_cache", _U8, 4),
+                      (v_cache, "v_cache", _U8, 4), (page_table, "page_table", _I32, 2),
+                      (seq_lens, "seq_lens", _I32, 1), (rel_logits, "rel_logits", _F32, 3),
+                      (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
+    workspace, ws_bytes = _workspace(
+        workspace, lambda: prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len), q)
+    _launch("inkling_rel_attn_prefill_q4", dev, stream,
             q.data_ptr(), cu_seqlens_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
             max_q_len, H_q, H_kv, D, P, n, rel_logits.shape[2], window, scale, max_seq_len, out.data_ptr(),
-            lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _ptr(device_error))
+            lse.data_ptr(), workspace.data_ptr(), ws_bytes, _error_word(device_error, dev))
     return out, lse
 
 
