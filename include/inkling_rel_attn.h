@@ -379,7 +379,7 @@ int inkling_rel_attn_build_tables(
  *                 it).  Negative: the token is skipped.  Past the pool:
  *                 INKLING_DEVERR_BAD_PAGE, skipped.  Slots of one call must be
  *                 distinct (two tokens of one slot leave a mixture of both)
- * No other byte of the cache is written.
+ * No other byte of the cache is written.  H_kv <= 65535.
  */
 int inkling_rel_attn_kv_append_q4(
     const void* k_new, const void* v_new, const int64_t* slot_map, int32_t T,

@@ -42,7 +42,7 @@ int rows_q4(bool append, void* k_rows, void* v_rows, const int64_t* slot_map, in
             int32_t page_size, int32_t num_pages, void* k_cache, void* v_cache, int32_t* device_error,
             void* stream) {
   if (T < 0 || !cache_shape_ok(H_kv, D, page_size, num_pages)) return INKLING_ERR_ARG;
-  if ((int64_t)H_kv * (D / 8) > INT32_MAX) return INKLING_ERR_ARG;
+  if (H_kv > 65535) return INKLING_ERR_ARG;  // heads are a dimension of the grid
   if (T == 0) return INKLING_OK;
   if (!k_rows || !v_rows || !slot_map || !k_cache || !v_cache) return INKLING_ERR_ARG;
   if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||

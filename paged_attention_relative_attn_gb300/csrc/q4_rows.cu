@@ -7,7 +7,9 @@
 // All three move rows and are bound by HBM.  A thread owns 8 adjacent channels
 // of K and the same 8 of V: 16 bytes each on the bf16 side, one 32-bit word
 // each on the 4-bit side; 4 adjacent lanes share a group and its scale, D / 8
-// lanes a row.  Reads and writes of a row's 4-bit side are D / 2 contiguous bytes.
+// lanes a row.  A block of the grid has one KV head of 2048 / D adjacent tokens:
+// its rows follow from the thread's number without a division, and tokens that
+// are neighbours in the cache, as a chunk's are, fill whole blocks of it.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,8 +28,16 @@ struct Q4RowsParams {
   uint8_t* v_cache;
   const int64_t* slots;
   int32_t* dev_err;
+  uint64_t inv_P;  // 2^64 / P rounded up: slots below 2^31 * 256 divide by the high half of a product
   int T, H_kv, P, num_pages;
 };
+
+__device__ __forceinline__ size_t q4_slot_at(const Q4RowsParams& p, int64_t slot, int h, int D, int& r) {
+  const int page = (int)__umul64hi((uint64_t)slot, p.inv_P);
+  const int place = (int)(slot - (int64_t)page * p.P);
+  r = place % kQ4Block;
+  return q4_block_at(page, h, place, p.H_kv, p.P, D);
+}
 
 // Word of a V row that this lane stores: lane i (group j = i / 4, t = i % 4)
 // holds the 16-bit units (g = 2t, j) and (2t + 1, j) of the row; a word has the
@@ -48,20 +58,16 @@ __global__ void __launch_bounds__(kRowThreads)
     kv_append_q4_kernel(const __grid_constant__ Q4RowsParams p) {
   constexpr int N = D / kQ4Group;
   constexpr int U = D / 8;  // lanes per row
-  const int per_token = p.H_kv * U;
-  const size_t idx = (size_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const size_t total = (size_t)p.T * per_token;
-  const bool in = idx < total;  // total is a multiple of 8: lanes that exchange are in or out together
-  const int t_row = in ? (int)(idx / per_token) : 0;
-  const int u = (int)(idx - (size_t)t_row * per_token);
+  const int t_row = blockIdx.x * (kRowThreads / U) + threadIdx.x / U, h = blockIdx.y;
+  const int i = threadIdx.x % U, j = i >> 2, t = i & 3;
   uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
   int64_t slot = -1;
-  if (in) {
+  if (t_row < p.T) {
+    const size_t idx = ((size_t)t_row * p.H_kv + h) * U + i;
+    slot = __ldg(p.slots + t_row);
     kr = __ldcs(p.k_rows + idx);
     vr = __ldcs(p.v_rows + idx);
-    slot = __ldg(p.slots + t_row);
   }
-  const int h = u / U, i = u % U, j = i >> 2, t = i & 3;
   uint32_t ks, vs;
   const uint32_t kw = q4_quantise8(kr, ks);
   const uint32_t vw = v_swap(q4_quantise8(vr, vs), j);
@@ -70,9 +76,8 @@ __global__ void __launch_bounds__(kRowThreads)
     report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
     return;
   }
-  const int page = (int)(slot / p.P), place = (int)(slot - (int64_t)page * p.P);
-  const size_t at = q4_block_at(page, h, place, p.H_kv, p.P, D);
-  const int r = place % kQ4Block;
+  int r;
+  const size_t at = q4_slot_at(p, slot, h, D, r);
   uint8_t* kb = p.k_cache + at;
   uint8_t* vb = p.v_cache + at;
   reinterpret_cast<uint32_t*>(kb + r * (D / 2))[N * t + j] = kw;
@@ -83,42 +88,41 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// The 8 K and 8 V channels (group j, quarter t) of row r of the blocks at kb, vb, as bf16.
+// The 8 K and 8 V channels (group j, quarter t) of row r of the blocks at kb, vb, as bf16;
+// zeros without a block.  All lanes of a warp call it together (V words are swapped).
 template <int D>
-__device__ __forceinline__ void q4_read8(const uint8_t* kb, const uint8_t* vb, int r, int j, int t,
+__device__ __forceinline__ void q4_read8(const uint8_t* kb, const uint8_t* vb, bool have, int r, int j, int t,
                                          uint4& k, uint4& v) {
   constexpr int N = D / kQ4Group;
-  const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(kb + r * (D / 2)) + N * t + j);
-  const uint16_t* vrow = reinterpret_cast<const uint16_t*>(vb + r * (D / 2));
-  const uint32_t vw = (uint32_t)__ldg(vrow + N * (2 * t) + j) |
-                      ((uint32_t)__ldg(vrow + N * (2 * t + 1) + j) << 16);
-  const float ks = __uint_as_float(
-      (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(kb + q4_scale_off(D)) + r * N + j) << 16);
-  const float vs = __uint_as_float(
-      (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(vb + q4_scale_off(D)) + r * N + j) << 16);
-  k = make_uint4(q4_value2(kw, 0, ks), q4_value2(kw, 1, ks), q4_value2(kw, 2, ks), q4_value2(kw, 3, ks));
-  v = make_uint4(q4_value2(vw, 0, vs), q4_value2(vw, 1, vs), q4_value2(vw, 2, vs), q4_value2(vw, 3, vs));
+  uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
+  if (have) {
+    kw = __ldg(reinterpret_cast<const uint32_t*>(kb + r * (D / 2)) + N * t + j);
+    vw = __ldg(reinterpret_cast<const uint32_t*>(vb + r * (D / 2)) + v_word<D>(j, t));
+    ks = __ldg(reinterpret_cast<const uint16_t*>(kb + q4_scale_off(D)) + r * N + j);
+    vs = __ldg(reinterpret_cast<const uint16_t*>(vb + q4_scale_off(D)) + r * N + j);
+  }
+  k = q4_values8(kw, ks);
+  v = q4_values8(v_swap(vw, j), vs);
+  if (!have) k = v = make_uint4(0, 0, 0, 0);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     kv_read_q4_kernel(const __grid_constant__ Q4RowsParams p) {
   constexpr int U = D / 8;
-  const int per_token = p.H_kv * U;
-  const size_t idx = (size_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (idx >= (size_t)p.T * per_token) return;
-  const int t_row = (int)(idx / per_token);
-  const int u = (int)(idx - (size_t)t_row * per_token);
-  const int64_t slot = __ldg(p.slots + t_row);
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  const int t_row = blockIdx.x * (kRowThreads / U) + threadIdx.x / U, h = blockIdx.y;
+  const int i = threadIdx.x % U;
+  int64_t slot = t_row < p.T ? __ldg(p.slots + t_row) : -1;
   if (slot >= (int64_t)p.num_pages * p.P) {
     report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
-  } else if (slot >= 0) {
-    const int page = (int)(slot / p.P), place = (int)(slot - (int64_t)page * p.P);
-    const int h = u / U, i = u % U;
-    const size_t at = q4_block_at(page, h, place, p.H_kv, p.P, D);
-    q4_read8<D>(p.k_cache + at, p.v_cache + at, place % kQ4Block, i >> 2, i & 3, k, v);
+    slot = -1;
   }
+  int r = 0;
+  const size_t at = slot >= 0 ? q4_slot_at(p, slot, h, D, r) : 0;
+  uint4 k, v;
+  q4_read8<D>(p.k_cache + at, p.v_cache + at, slot >= 0, r, i >> 2, i & 3, k, v);
+  if (t_row >= p.T) return;
+  const size_t idx = ((size_t)t_row * p.H_kv + h) * U + i;
   p.k_rows[idx] = k;
   p.v_rows[idx] = v;
 }
@@ -135,15 +139,14 @@ static Q4RowsParams rows_params(const Q4RowsCall& c) {
   p.H_kv = c.H_kv;
   p.P = c.P;
   p.num_pages = c.num_pages;
+  p.inv_P = ~0ull / (uint64_t)c.P + 1;  // P >= 16: exact for powers of two, rounded up for the others
   return p;
 }
 
 int launch_q4_rows(const Q4RowsCall& c, bool append) {
   const Q4RowsParams p = rows_params(c);
-  const int64_t units = (int64_t)c.T * c.H_kv * (c.D / 8);
-  const int64_t blocks = (units + kRowThreads - 1) / kRowThreads;
-  if (blocks > INT32_MAX) return INKLING_ERR_ARG;
-  const unsigned g = (unsigned)blocks;
+  const int per_block = kRowThreads / (c.D / 8);
+  const dim3 g((unsigned)(((int64_t)c.T + per_block - 1) / per_block), (unsigned)c.H_kv);
   if (append) {
     if (c.D == 128) kv_append_q4_kernel<128><<<g, kRowThreads, 0, c.stream>>>(p);
     else kv_append_q4_kernel<64><<<g, kRowThreads, 0, c.stream>>>(p);
@@ -204,18 +207,24 @@ __global__ void __launch_bounds__(kRowThreads)
   const int page = __ldg(p.page_table + (size_t)b * p.pt_stride + lp);
   const bool ok = page >= 0 && page < p.num_pages;
   if (!ok && threadIdx.x == 0) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
-  const int n = min(kExpandTokens, L - j0) * p.H_kv * U;
-  const size_t dst0 = ((size_t)b * p.pages_per_seq * 64 + (j0 - base)) * p.H_kv * U;
-  for (int x = threadIdx.x; x < n; x += kRowThreads) {
-    const int r = x / (p.H_kv * U), u = x - r * (p.H_kv * U);
-    const int h = u / U, i = u % U;
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    if (ok) {
-      const size_t at = q4_block_at(page, h, j0 - lp * p.P, p.H_kv, p.P, D);
-      q4_read8<D>(p.k_cache + at, p.v_cache + at, r, i >> 2, i & 3, k, v);
+  // thread: 8 channels of one row, head after head (with D = 64 half of the block has every other head)
+  constexpr int kHeads = kRowThreads / (kExpandTokens * U);
+  const int i = threadIdx.x % U, r = threadIdx.x / U % kExpandTokens;
+  const bool in = r < L - j0;
+  const size_t block = q4_block_at(0, 1, 0, 1, p.P, D);  // from one head's first block to the next's
+  const size_t at = q4_block_at(ok ? page : 0, 0, j0 - lp * p.P, p.H_kv, p.P, D);
+  const size_t dst = ((size_t)b * p.pages_per_seq * 64 + (j0 - base) + r) * p.H_kv * U + i;
+#pragma unroll 4
+  for (int h0 = 0; h0 < p.H_kv; h0 += kHeads) {
+    const int h = h0 + threadIdx.x / (kExpandTokens * U);
+    const bool mine = in && h < p.H_kv;
+    const size_t src = at + (size_t)h * block;
+    uint4 k, v;
+    q4_read8<D>(p.k_cache + src, p.v_cache + src, ok && mine, r, i >> 2, i & 3, k, v);
+    if (mine) {
+      p.k_out[dst + (size_t)h * U] = k;
+      p.v_out[dst + (size_t)h * U] = v;
     }
-    p.k_out[dst0 + x] = k;
-    p.v_out[dst0 + x] = v;
   }
 }
 
