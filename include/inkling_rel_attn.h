@@ -339,7 +339,8 @@ int inkling_rel_attn_kv_conv_append(
  * outside [0, num_pages) on the stack set INKLING_DEVERR_BAD_PAGE and give slot
  * -1, and so does a stack that would grow past num_pages (the pages past it are
  * dropped); more new tokens than max_tokens set INKLING_DEVERR_BAD_CHUNK (the
- * tokens past it get no slot).  B <= 8192, page_size as everywhere.
+ * tokens past it get no slot).  B <= 8192 (0: nothing is written), page_size as
+ * everywhere, num_pages and max_tokens below 2^31 - 1.
  */
 int inkling_rel_attn_build_tables(
     const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_table,

@@ -74,9 +74,9 @@ int inkling_rel_attn_build_tables(const int32_t* seq_lens, const int32_t* new_le
                                   int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
                                   int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
                                   int32_t* free_left, int32_t* device_error, void* stream) {
-  if (B < 0 || B > kTablesMaxBatch || max_tokens < 0) return INKLING_ERR_ARG;
+  if (B < 0 || B > kTablesMaxBatch || max_tokens < 0 || max_tokens == INT32_MAX) return INKLING_ERR_ARG;
   if (page_size <= 0 || page_size % 16 != 0 || page_size > 256) return INKLING_ERR_ARG;
-  if (num_pages <= 0 || page_table_stride <= 0) return INKLING_ERR_ARG;
+  if (num_pages <= 0 || num_pages == INT32_MAX || page_table_stride <= 0) return INKLING_ERR_ARG;
   if ((int64_t)page_table_stride * page_size > INT32_MAX) return INKLING_ERR_ARG;
   if (B == 0) return INKLING_OK;
   if (!seq_lens || !new_lens || !page_table || !free_pages || !free_count || !kv_lens || !cu_seqlens_q ||
