@@ -14,14 +14,17 @@
 // block, and a second kernel joins them.  The cuts depend on the lengths alone, not
 // on page ids or timing.
 //
-// A thread block has a producer warp and four consumer warps.  The producer walks
-// the run, looks pages up and brings each tile's K and V (9 D bytes per block each,
-// contiguous) into a ring of slots by bulk copy, a lane per tile; the ring runs
-// across items, so the next one streams in while the current one is finished.  It
-// also prepares the items: q as operands, bias pointers and positions per lane.
-// Consumer warp w takes the ring's tiles w, w + 4, ... with an online softmax of
-// its own; at the item's end it leaves (m, l, O) in one of two shared-memory
-// buffers and goes on, and the last of the warps to do so adds the parts up.
+// A thread block has two producer warps and four consumer warps.  One producer
+// walks the run, looks pages up and brings each tile's K and V (9 D bytes per block
+// each, contiguous) into a ring of slots by bulk copy, a lane per tile; the ring runs
+// across items, so the next one streams in while the current one is finished.  The
+// other prepares the items (q as operands, bias pointers and positions per lane),
+// three ahead.  Consumer warp w takes the ring's tiles w, w + 4, ... with an online
+// softmax of its own; at the item's end it leaves (m, l, O) in one of two
+// shared-memory buffers and goes on, and the preparing warp adds the parts up.  (One
+// producer, and the last consumer to leave its part adding them up: 64 sequences of
+// 512 visible keys 36.9 us instead of 31.9, for the copies stalled at every item
+// and the slowest consumer was held up further.)
 // Four warps load the SM's four schedulers alike (six, which give two of them two
 // thirds of the work, took 195 us where four took 182), and a consumer's loop has
 // no second copy for masked tiles (instruction fetches count in a short call).
@@ -60,7 +63,7 @@ constexpr int kDq4SmemPerSm = 222 * 1024;
 constexpr float kDq4Slack = 5.5f;     // scores may exceed the exponent base by e^5.5 before it moves
 constexpr int kDq4W = 4;              // consumer warps
 constexpr int kDq4Ctas = 2;           // thread blocks per SM
-constexpr int kDq4Threads = 32 * (kDq4W + 1);
+constexpr int kDq4Threads = 32 * (kDq4W + 2);
 constexpr int kDq4U = 2;              // 16-token blocks per tile
 constexpr int kDq4Tile = 16 * kDq4U;  // keys per tile
 constexpr int kDq4Rows = 8;           // rows of an item at most: the N of an MMA
@@ -116,7 +119,7 @@ struct Dq4Smem {
     comb_off = item_off + kDq4ItemSlots * item_bytes;
     comb_floats = kDq4W * NR * (D + 4) + 2 * kDq4W * kDq4Rows;
     bar_off = comb_off + 2 * comb_floats * 4;
-    total = bar_off + (2 * slots + 2 * kDq4ItemSlots + 2) * 8 + 16;
+    total = bar_off + (2 * slots + 2 * kDq4ItemSlots + 4) * 8 + 16;
   }
 };
 
@@ -199,9 +202,9 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   uint64_t* empty = full + slots;
   uint64_t* ifull = empty + slots;           // items: published,
   uint64_t* iempty = ifull + kDq4ItemSlots;  // taken by every consumer
-  uint64_t* cempty = iempty + kDq4ItemSlots; // parts of an item: added up
-  int* arrived = reinterpret_cast<int*>(cempty + 2);  // warps that have left theirs
-  volatile int* abort_flag = arrived + 2;
+  uint64_t* cfull = iempty + kDq4ItemSlots;  // parts of an item: left by every consumer,
+  uint64_t* cempty = cfull + 2;              // added up
+  volatile int* abort_flag = reinterpret_cast<int*>(cempty + 2);
   auto item_at = [&](int s) { return smem + S.item_off + s * S.item_bytes; };
   auto item_rec = [&](int s) { return reinterpret_cast<Dq4Item*>(item_at(s)); };
   // token of row r of an item of so many heads, and its packed row
@@ -225,8 +228,8 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       mbar_init(smem_u32(iempty + i), W);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(cfull + i), W);
       mbar_init(smem_u32(cempty + i), 1);
-      arrived[i] = 0;
     }
     *abort_flag = 0;
   }
@@ -237,13 +240,15 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // =================================================================== producer
-  if (warp == W) {
+  // =================================================================== producers
+  // Both walk the run: warp W sends the tiles, warp W + 1 prepares the items.
+  if (warp >= W) {
+    const bool copier = warp == W;
     // ---- this thread block's run [x, x1) of the batch's tiles
     int64_t total = 0;
     for (int b = lane; b < p.B; b += 32) {
       total += (int64_t)p.H_kv * head_tiles(p, b);
-      if (blockIdx.x == 0) {
+      if (copier && blockIdx.x == 0) {
         const int Lr = __ldg(p.seq_lens + b);
         if (Lr > p.pt_stride * p.P) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
         if (p.QL > 1 && Lr < p.QL) report(p.dev_err, INKLING_DEVERR_BAD_CHUNK);
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       while (off >= group_range(p, L, grp).ntile) off -= group_range(p, L, grp++).ntile;
     }
 
-    int ki = 0, kb = 0;  // items and tiles published
+    int ki = 0, kb = 0;  // items published, tiles sent
     const int blocks_per_page = p.P / 16;
     const int batch = min(32, slots);
     uint32_t sent = 0;  // on a time-out: the copies of the batch at kb that went out
@@ -344,6 +349,51 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 #pragma unroll
       for (int i = 0; i < 3; ++i) dst[32 * i] = src[i];
     };
+    // ---- the sum of the warps' parts of an item
+    auto join = [&](const Dq4Item& it, int cb) {
+      constexpr int LR = D / 4;  // lanes per row
+      const float* co = comb_o(cb);
+      const float* cm = comb_m(cb);
+      const int rows = it.tn * it.heads, d = 4 * (lane % LR);
+#pragma unroll 1
+      for (int r = lane / LR; r < rows; r += 32 / LR) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, cm[w * HP + r]);
+        const float base = M == -INFINITY ? 0.f : M;
+        float l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float f = ex2((cm[w * HP + r] - base) * kLog2e);
+          const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + r) * OP + d);
+          l = fmaf(f, cm[(W + w) * HP + r], l);
+          a.x = fmaf(f, v.x, a.x);
+          a.y = fmaf(f, v.y, a.y);
+          a.z = fmaf(f, v.z, a.z);
+          a.w = fmaf(f, v.w, a.w);
+        }
+        if (it.part < 0) {
+          const size_t row = row_of(it, r);
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // every score -inf: an empty row
+          *reinterpret_cast<uint2*>(p.out + row * D + d) =
+              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+          if (d == 0 && p.lse_out) p.lse_out[row] = M + logf(l);
+        } else {
+          const size_t row = ((size_t)blockIdx.x * 2 + it.part) * NR + r;
+          *reinterpret_cast<float4*>(p.part_o + row * D + d) = a;
+          if (d == 0) p.part_ml[row] = make_float2(M, l);
+        }
+      }
+    };
+    auto join_item = [&](int k) -> bool {
+      const int cb = k & 1;
+      if (!waitw(smem_u32(cfull + cb), (k >> 1) & 1, abort_flag)) return false;
+      join(*item_rec(k % kDq4ItemSlots), cb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
+      return true;
+    };
     auto publish = [&](const Dq4Item& it) -> bool {
       const int s = ki % kDq4ItemSlots;
       bool good = true;
@@ -377,7 +427,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
           cut = make_int4(it.row0, it.tn, last - (int)blockIdx.x + 1, it.heads);
         }
       }
-      if (p.bias_prefetch && lane < it.tn * it.heads) {  // this row's bias for the part's keys
+      if (!copier && p.bias_prefetch && lane < it.tn * it.heads) {  // this row's bias for the part's keys
         const int pr = it.pos0 + token_of(lane, it.heads);
         const int far = pr - TK * it.tile0, near = pr - (TK * (it.tile0 + it.ntile) - 1);
         const int dlo = min(max(near, 0), p.R - 1) & ~3;
@@ -385,9 +435,8 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
         const float* row = p.rel + row_of(it, lane) * p.R;
         if (dhi > dlo) bulk_prefetch_l2(row + dlo, (uint32_t)(dhi - dlo) * 4);
       }
-      // the first item's tiles are sent for before it is prepared
-      bool published = ki > 0;
-      if (published) ok = publish(it);
+      // (the record of item ki - 2 is in the slot of the item after this one)
+      if (!copier) ok = publish(it) && (ki < 3 || join_item(ki - 3));
       if (!ok) break;
       // ---- its tiles: a lane each, a batch of at most 32 (and of the ring's slots: no
       // two lanes share one) at a time.  A lane's copies go out as soon as its slot is
@@ -396,13 +445,13 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       const int pos1 = it.pos0 + it.tn - 1;
       auto page_of = [&](int i, int u) -> int {  // page of block u of tile i; -1: past the last key
         const int key = (it.tile0 + i) * TK + 16 * u;
-        return lane < batch && i < it.ntile && (u == 0 || key <= pos1) ? __ldg(pt_row + key / p.P) : -1;
+        return copier && lane < batch && i < it.ntile && (u == 0 || key <= pos1) ? __ldg(pt_row + key / p.P) : -1;
       };
       int page[U], next[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) next[u] = page_of(lane, u);
 #pragma unroll 1
-      for (int i0 = 0; i0 < it.ntile; i0 += batch) {
+      for (int i0 = 0; copier && i0 < it.ntile; i0 += batch) {
         const int i = i0 + lane, key0 = (it.tile0 + i) * TK;
         int place[U];
         bool fine[U];
@@ -467,11 +516,6 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
           break;
         }
         kb += min(batch, it.ntile - i0);
-        if (!published) {
-          ok = publish(it);
-          published = true;
-          if (!ok) break;
-        }
       }
       if (!ok) break;
       // ---- the next item
@@ -488,12 +532,18 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
         }
       }
     }
-    if (ok) {
-      Dq4Item end;
-      memset(&end, 0, sizeof(end));
-      ok = publish(end);  // ntile = 0: no more items
+    if (!copier) {
+      if (ok) {
+        Dq4Item end;
+        memset(&end, 0, sizeof(end));
+        const int n = ki;
+        ok = publish(end) && (n < 2 || join_item(n - 2)) && (n < 1 || join_item(n - 1));  // ntile = 0: no more items
+      }
+      if (lane == 0) p.cut[blockIdx.x] = cut;
+      if (!ok && lane == 0) report(p.dev_err, INKLING_DEVERR_TIMEOUT);
+      return;
     }
-    if (lane == 0) p.cut[blockIdx.x] = cut;
+    ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
     if (!ok) {  // drain: each slot's last copy in flight, which nobody reads
       for (int j = lane; j < slots; j += 32) {
         int n = kb - kb % slots + j;  // the slot's tile in [kb, kb + slots), or before
@@ -528,44 +578,6 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   const int row_k = key_g * (D / 2) + 4 * N * t;                 // this lane's part of a K row
   const int row_v0 = t * (D / 2) + 2 * N * g, row_v1 = (4 + (t ^ 1)) * (D / 2) + 2 * N * g;  // and of V rows
   const int row_s = q4_scale_off(D) + key_g * (2 * N);           // and of the scales
-
-  // ---- the sum of the warps' parts of an item
-  auto join = [&](const Dq4Item& it, int cb) {
-    constexpr int LR = D / 4;  // lanes per row
-    const float* co = comb_o(cb);
-    const float* cm = comb_m(cb);
-    const int rows = it.tn * it.heads, d = 4 * (lane % LR);
-#pragma unroll 1
-    for (int r = lane / LR; r < rows; r += 32 / LR) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, cm[w * HP + r]);
-      const float base = M == -INFINITY ? 0.f : M;
-      float l = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = ex2((cm[w * HP + r] - base) * kLog2e);
-        const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + r) * OP + d);
-        l = fmaf(f, cm[(W + w) * HP + r], l);
-        a.x = fmaf(f, v.x, a.x);
-        a.y = fmaf(f, v.y, a.y);
-        a.z = fmaf(f, v.z, a.z);
-        a.w = fmaf(f, v.w, a.w);
-      }
-      if (it.part < 0) {
-        const size_t row = row_of(it, r);
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // every score -inf: an empty row
-        *reinterpret_cast<uint2*>(p.out + row * D + d) =
-            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-        if (d == 0 && p.lse_out) p.lse_out[row] = M + logf(l);
-      } else {
-        const size_t row = ((size_t)blockIdx.x * 2 + it.part) * NR + r;
-        *reinterpret_cast<float4*>(p.part_o + row * D + d) = a;
-        if (d == 0) p.part_ml[row] = make_float2(M, l);
-      }
-    }
-  };
 
   int kb_w = 0;       // tiles of the items before this one, modulo W
   int s_slot = warp;  // this warp's next slot (it owns warp, warp + W, ...) and its phase
@@ -835,7 +847,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
     }
     if (!ok) break;
 
-    // ---- this warp's part of the item; the last one adds them up
+    // ---- this warp's part of the item
     const int cb = ki & 1;
     if (ki >= 2 && !waitw(smem_u32(cempty + cb), ((ki >> 1) - 1) & 1, abort_flag)) {
       ok = false;
@@ -860,18 +872,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       }
     }
     __syncwarp();
-    int before = 0;
-    if (lane == 0) {
-      __threadfence_block();
-      before = atomicAdd(arrived + cb, 1);
-      if (before == W - 1) arrived[cb] = 0;  // nobody adds to it before cempty
-      __threadfence_block();
-    }
-    if (__shfl_sync(0xffffffffu, before, 0) == W - 1) {
-      join(it, cb);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
-    }
+    if (lane == 0) mbar_arrive(smem_u32(cfull + cb));
   }
   if (!ok && lane == 0) report(p.dev_err, INKLING_DEVERR_TIMEOUT);
 }
