@@ -64,6 +64,7 @@ constexpr float kDq4Slack = 5.5f;     // scores may exceed the exponent base by 
 constexpr int kDq4W = 4;              // consumer warps
 constexpr int kDq4Ctas = 2;           // thread blocks per SM
 constexpr int kDq4Threads = 32 * (kDq4W + 2);
+constexpr int kDq4MergeWarps = 4;     // of the joining kernel's blocks: a thread per channel in all
 constexpr int kDq4U = 2;              // 16-token blocks per tile
 constexpr int kDq4Tile = 16 * kDq4U;  // keys per tile
 constexpr int kDq4Rows = 8;           // rows of an item at most: the N of an MMA
@@ -880,25 +881,41 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 // ---------------------------------------------------------------------------
 // Joins the parts of cut items: block (c, r) has row r of the item that thread
 // block c's run cuts first.  Its parts are c's second and the first of c + 1 .. ;
-// 8 warps take them in turn, D / 32 channels per lane.
+// the block's warps take them in turn, D / 32 channels per lane.
 template <int D>
-__global__ void __launch_bounds__(256) merge_q4_kernel(const __grid_constant__ DecodeQ4Params p) {
+__global__ void __launch_bounds__(32 * kDq4MergeWarps) merge_q4_kernel(const __grid_constant__ DecodeQ4Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int C = D / 32;
   const int4 cut = p.cut[blockIdx.x];
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (cut.z == 0 || r >= cut.y * cut.w) return;
-  __shared__ float s_o[8][D];
-  __shared__ float2 s_ml[8];
+  __shared__ float s_o[kDq4MergeWarps][D];
+  __shared__ float2 s_ml[kDq4MergeWarps];
   auto part_row = [&](int k) {
     return ((size_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * p.NR + r;
   };
+  // a warp's first part is asked for along with the record that says whether there is
+  // one (its place in the workspace exists in any case)
   float M = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  if (blockIdx.x + warp < gridDim.x) {
+    const size_t row = part_row(warp);
+    const float2 ml = p.part_ml[row];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = p.part_o[row * D + lane + 32 * c];
+    M = ml.x;
+    l = ml.y;
+  }
+  if (cut.z == 0 || r >= cut.y * cut.w) return;
+  if (warp >= cut.z) {
+    M = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  }
 #pragma unroll 4
-  for (int k = warp; k < cut.z; k += 8) {
+  for (int k = warp + kDq4MergeWarps; k < cut.z; k += kDq4MergeWarps) {
     const size_t row = part_row(k);
     const float2 ml = p.part_ml[row];
     float v[C];
@@ -919,12 +936,12 @@ __global__ void __launch_bounds__(256) merge_q4_kernel(const __grid_constant__ D
   const int d = threadIdx.x;
   M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_ml[w].x);
+  for (int w = 0; w < kDq4MergeWarps; ++w) M = fmaxf(M, s_ml[w].x);
   const float base = M == -INFINITY ? 0.f : M;
   float o = 0.f;
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kDq4MergeWarps; ++w) {
     const float f = ex2((s_ml[w].x - base) * kLog2e);
     l = fmaf(s_ml[w].y, f, l);
     o = fmaf(s_o[w][d], f, o);
@@ -988,7 +1005,7 @@ static int launch_decode_q4_t(const DecodeQ4Call& c, DecodeQ4Params prm, const D
   static std::atomic<int> limit_set[kMaxDevices];
   if (!smem_limit_on_device(reinterpret_cast<const void*>(kern), budget, limit_set)) return INKLING_ERR_CUDA;
   if (!launch_dependent(kern, dim3(plan.grid), kDq4Threads, smem, prm, c.stream)) return INKLING_ERR_CUDA;
-  if (!launch_dependent(merge_q4_kernel<D>, dim3(plan.grid, plan.NR), 256, 0, prm, c.stream))
+  if (!launch_dependent(merge_q4_kernel<D>, dim3(plan.grid, plan.NR), 32 * kDq4MergeWarps, 0, prm, c.stream))
     return INKLING_ERR_CUDA;
   return INKLING_OK;
 }
