@@ -644,17 +644,13 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       // ---- bias, on its way while the tile is awaited and K multiplied
       const bool inside = key0 + TK - 1 <= pos0 && (p.window <= 0 || pos1 - key0 < p.window);
       float bv[U][4];
-      if (inside && pos0 - (key0 + TK - 1) >= p.R - 1) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) bv[u][x] = pr.far[x & 1];
-      } else if (inside && pos1 - key0 < p.R) {
+      const bool far = inside && pos0 - (key0 + TK - 1) >= p.R - 1;
+      if (!far && inside && pos1 - key0 < p.R) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int x = 0; x < 4; ++x) bv[u][x] = __ldg(pr.bias[x & 1] - key0 - 16 * u - 8 * (x >> 1));
-      } else {
+      } else if (!far) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -746,13 +742,20 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
           sc[u][3] = fmaf(c[3], s8, sc[u][3]);
         }
       }
+      if (far) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sc[u][x] = fmaf(sc[u][x], p.scale, bv[u][x]);
-          if constexpr (MULTI) sc[u][x] = bv[u][x] == -INFINITY ? -INFINITY : sc[u][x];  // its scale may be NaN
-        }
+          for (int x = 0; x < 4; ++x) sc[u][x] = fmaf(sc[u][x], p.scale, pr.far[x & 1]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            sc[u][x] = fmaf(sc[u][x], p.scale, bv[u][x]);
+            if constexpr (MULTI) sc[u][x] = bv[u][x] == -INFINITY ? -INFINITY : sc[u][x];  // its scale may be NaN
+          }
+      }
       // ---- running maximum and sum.  The maximum, the exponents' base, is
       // taken anew over the warp only when a score passes it by kDq4Slack;
       // until then a weight is at most e^kDq4Slack and nothing is rescaled.
