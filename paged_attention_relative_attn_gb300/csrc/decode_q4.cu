@@ -97,6 +97,7 @@ struct Dq4Item {
   int tn, heads, pos0;
   int tile0, ntile;
   int part;  // -1: the whole item; else its part number of this thread block
+  int inv;   // 256 / heads, rounded up: rows (below 8) divide by a product
 };
 
 // What the producer prepares of an item, per lane of a consumer.
@@ -208,10 +209,10 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   volatile int* abort_flag = reinterpret_cast<int*>(cempty + 2);
   auto item_at = [&](int s) { return smem + S.item_off + s * S.item_bytes; };
   auto item_rec = [&](int s) { return reinterpret_cast<Dq4Item*>(item_at(s)); };
-  // token of row r of an item of so many heads, and its packed row
-  auto token_of = [&](int r, int heads) { return MULTI ? r / heads : 0; };
+  // token of an item's row r, and its packed row
+  auto token_of = [&](const Dq4Item& it, int r) { return MULTI ? (r * it.inv) >> 8 : 0; };
   auto row_of = [&](const Dq4Item& it, int r) {
-    const int i = token_of(r, it.heads);
+    const int i = token_of(it, r);
     return (size_t)it.row0 + (size_t)i * p.H_q + (r - i * it.heads);
   };
   // Key of a block that MMA row g (and g + 8: 8 more) stands for: rows 2t, 2t + 1
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = min(2 * t + x, rows - 1);
-        pr.pos[x] = it.pos0 + token_of(r, it.heads);
+        pr.pos[x] = it.pos0 + token_of(it, r);
         const float* row = p.rel + row_of(it, r) * p.R;
         pr.bias[x] = row + (pr.pos[x] - key_g);
         pr.far[x] = it.pos0 + it.tn - 1 - TK * it.tile0 >= p.R ? __ldg(row + p.R - 1) : 0.f;
@@ -351,46 +352,56 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       for (int i = 0; i < 3; ++i) dst[32 * i] = src[i];
     };
     // ---- the sum of the warps' parts of an item
+    // lane W * r + w makes the factor of warp w's part of row r.  (Short code: this warp
+    // shares the instruction cache with the consumers' loop; unrolled by 4, 11 us more
+    // for 64 sequences of 4 drafts.)
     auto join = [&](const Dq4Item& it, int cb) {
+      static_assert(W * HP == 32, "a lane per row and warp");
       constexpr int LR = D / 4;  // lanes per row
       const float* co = comb_o(cb);
       const float* cm = comb_m(cb);
       const int rows = it.tn * it.heads, d = 4 * (lane % LR);
-#pragma unroll 1
-      for (int r = lane / LR; r < rows; r += 32 / LR) {
-        float M = -INFINITY;
+      const float m = cm[lane % W * HP + lane / W];
+      float M = m;
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, cm[w * HP + r]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float l = 0.f;
+      for (int off = 1; off < W; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      float f = ex2((m - (M == -INFINITY ? 0.f : M)) * kLog2e);
+      float l = f * cm[(W + lane % W) * HP + lane / W];
+#pragma unroll
+      for (int off = 1; off < W; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      const bool mine = lane % W == 0 && lane / W < rows;
+      if (it.part < 0) {
+        f *= l == 0.f ? 0.f : __fdividef(1.f, l);  // every score -inf: an empty row
+        if (mine && p.lse_out) p.lse_out[row_of(it, lane / W)] = M + logf(l);
+      } else if (mine) {
+        p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + lane / W] = make_float2(M, l);
+      }
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 32 / LR) {
+        const int r = r0 + lane / LR;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float f = ex2((cm[w * HP + r] - base) * kLog2e);
-          const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + r) * OP + d);
-          l = fmaf(f, cm[(W + w) * HP + r], l);
-          a.x = fmaf(f, v.x, a.x);
-          a.y = fmaf(f, v.y, a.y);
-          a.z = fmaf(f, v.z, a.z);
-          a.w = fmaf(f, v.w, a.w);
+          const float fw = __shfl_sync(0xffffffffu, f, min(W * r + w, 31));
+          const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + min(r, rows - 1)) * OP + d);
+          a.x = fmaf(fw, v.x, a.x);
+          a.y = fmaf(fw, v.y, a.y);
+          a.z = fmaf(fw, v.z, a.z);
+          a.w = fmaf(fw, v.w, a.w);
         }
-        if (it.part < 0) {
-          const size_t row = row_of(it, r);
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // every score -inf: an empty row
-          *reinterpret_cast<uint2*>(p.out + row * D + d) =
-              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-          if (d == 0 && p.lse_out) p.lse_out[row] = M + logf(l);
-        } else {
-          const size_t row = ((size_t)blockIdx.x * 2 + it.part) * NR + r;
-          *reinterpret_cast<float4*>(p.part_o + row * D + d) = a;
-          if (d == 0) p.part_ml[row] = make_float2(M, l);
-        }
+        if (r >= rows) continue;
+        if (it.part < 0)
+          *reinterpret_cast<uint2*>(p.out + row_of(it, r) * D + d) =
+              make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+        else
+          *reinterpret_cast<float4*>(p.part_o + (((size_t)blockIdx.x * 2 + it.part) * NR + r) * D + d) = a;
       }
     };
     auto join_item = [&](int k) -> bool {
       const int cb = k & 1;
       if (!waitw(smem_u32(cfull + cb), (k >> 1) & 1, abort_flag)) return false;
-      join(*item_rec(k % kDq4ItemSlots), cb);
+      const Dq4Item it = *item_rec(k % kDq4ItemSlots);
+      join(it, cb);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
       return true;
@@ -416,6 +427,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       it.row0 = (b * p.QL + grp / p.HG * p.TG) * p.H_q + hkv * p.G + h0;
       it.tn = r.tn;
       it.heads = min(p.HI, p.G - h0);
+      it.inv = 255 / it.heads + 1;
       it.pos0 = r.pos0;
       it.tile0 = r.tile0 + off;
       it.ntile = (int)min((int64_t)(r.ntile - off), x1 - x);
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
         }
       }
       if (!copier && p.bias_prefetch && lane < it.tn * it.heads) {  // this row's bias for the part's keys
-        const int pr = it.pos0 + token_of(lane, it.heads);
+        const int pr = it.pos0 + token_of(it, lane);
         const int far = pr - TK * it.tile0, near = pr - (TK * (it.tile0 + it.ntile) - 1);
         const int dlo = min(max(near, 0), p.R - 1) & ~3;
         const int dhi = min(min(max(far, 0), p.R - 1) + 4, p.R) & ~3;
