@@ -408,6 +408,9 @@ int inkling_rel_attn_kv_read_q4(
  *   The work is cut over the GPU by the batch's lengths, read on the device:
  * no host bound on them is needed, and results do not depend on page ids or
  * timing (they do depend, in the last bits, on the other lengths in the batch).
+ *   Range: |q| <= 2^60, and V groups whose largest magnitude lies in 2^-37 ..
+ * 2^57 (a group of smaller values is added with fewer bits, of larger ones may
+ * overflow); K groups may use the cache's whole range.
  *   workspace  inkling_rel_attn_decode_q4_workspace_size bytes, 16-byte aligned,
  *              no content expected or kept; calls that may overlap need one each
  */
