@@ -257,6 +257,7 @@ int inkling_rel_attn_prefill_q4(const void* q, const int32_t* cu_seqlens_q, cons
   c.lse_out = lse_out;
   c.dev_err = device_error;
   c.stream = static_cast<cudaStream_t>(stream);
+  c.after_expansion = true;
   return launch_prefill(c);
 }
 

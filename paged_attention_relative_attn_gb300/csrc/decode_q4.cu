@@ -50,6 +50,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "launch.h"
 #include "plan.cuh"
 #include "ptx.cuh"
 #include "q4.cuh"
@@ -237,10 +238,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   }
   fence_mbar_init();
   __syncthreads();
-  // launched with programmatic stream serialization: nothing of the previous
-  // kernel's is read or overwritten before it has completed
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_previous_kernel();
 
   // =================================================================== producers
   // Both walk the run: warp W sends the tiles, warp W + 1 prepares the items.
@@ -899,8 +897,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 // the block's warps take them in turn, D / 32 channels per lane.
 template <int D>
 __global__ void __launch_bounds__(32 * kDq4MergeWarps) merge_q4_kernel(const __grid_constant__ DecodeQ4Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  await_previous_kernel();
   constexpr int C = D / 32;
   const int4 cut = p.cut[blockIdx.x];
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -989,22 +986,6 @@ struct Dq4Plan {
 
 size_t decode_q4_workspace_bytes(int32_t, int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms) {
   return Dq4Plan(QL, H_q, H_kv, D, sms).total;
-}
-
-template <typename K>
-static bool launch_dependent(K kern, dim3 grid, int threads, int smem, const DecodeQ4Params& prm,
-                             cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, prm) == cudaSuccess && cudaGetLastError() == cudaSuccess;
 }
 
 template <int D, bool MULTI>

@@ -76,6 +76,7 @@ struct PrefillCall {
   float* lse_out;
   int32_t* dev_err;
   cudaStream_t stream;
+  bool after_expansion = false;  // set up while the expansion of the 4-bit cache ends
 };
 
 struct KvAppendCall {

@@ -53,6 +53,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "launch.h"
 #include "plan.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   // a sequence's query tiles run last tile first: later tiles see more keys,
   // so a call ends on its shortest CTAs
   const int qt = p.tiles_per_seq - 1 - (int)(blockIdx.y - b * p.tiles_per_seq);
+  await_previous_kernel();
   if (b >= p.B) return;
 
   // ---- the sequence's scalars, loaded together; their latency overlaps the
@@ -850,6 +852,8 @@ static int launch_prefill_t(const PrefillCall& c, const PrefillParams& prm, dim3
   static std::atomic<int> limit_set[kMaxDevices];
   if (!smem_limit_on_device(reinterpret_cast<const void*>(kern), smem, limit_set))
     return INKLING_ERR_CUDA;
+  if (c.after_expansion)
+    return launch_dependent(kern, grid, kPrefThreads, smem, prm, c.stream) ? INKLING_OK : INKLING_ERR_CUDA;
   kern<<<grid, kPrefThreads, smem, c.stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return INKLING_ERR_CUDA;
   return INKLING_OK;

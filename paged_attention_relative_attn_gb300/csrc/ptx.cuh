@@ -26,6 +26,13 @@ __device__ __forceinline__ unsigned long long globaltimer() {
   return t;
 }
 
+// For kernels launched with launch_dependent: nothing of the previous kernel's is
+// read or overwritten before the wait is over; the next one may be set up from now on.
+__device__ __forceinline__ void await_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -14,13 +14,15 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "launch.h"
 #include "plan.cuh"
+#include "ptx.cuh"
 #include "q4.cuh"
 
 namespace ira {
 
 constexpr int kRowThreads = 256;
-constexpr int kQ4Heads = 2;           // heads per thread of a large call (8192 tokens x 16 heads both ways: 30.2 us; 1: 33.7, 4: 31.9)
+constexpr int kQ4Heads = 2;           // heads per thread of a large call (8192 tokens x 16 heads both ways: 30 us; 1: 33.7, 4: 31.9)
 constexpr int kRowsFill = 152 * 4;    // blocks that give every SM some
 
 struct Q4RowsParams {
@@ -58,6 +60,7 @@ __device__ __forceinline__ uint32_t v_swap(uint32_t units, int j) {
 template <int D, int HEADS>
 __global__ void __launch_bounds__(kRowThreads)
     kv_append_q4_kernel(const __grid_constant__ Q4RowsParams p) {
+  await_previous_kernel();
   constexpr int N = D / kQ4Group;
   constexpr int U = D / 8;  // lanes per row
   const int t_row = blockIdx.x * (kRowThreads / U) + threadIdx.x / U, h0 = blockIdx.y * HEADS;
@@ -119,6 +122,7 @@ __device__ __forceinline__ void q4_read8(const uint8_t* kb, const uint8_t* vb, b
 template <int D, int HEADS>
 __global__ void __launch_bounds__(kRowThreads)
     kv_read_q4_kernel(const __grid_constant__ Q4RowsParams p) {
+  await_previous_kernel();
   constexpr int U = D / 8;
   const int t_row = blockIdx.x * (kRowThreads / U) + threadIdx.x / U, h0 = blockIdx.y * HEADS;
   const int i = threadIdx.x % U;
@@ -162,11 +166,11 @@ static Q4RowsParams rows_params(const Q4RowsCall& c) {
 }
 
 template <int D, int HEADS>
-static void rows_launch(const Q4RowsParams& p, bool append, cudaStream_t stream) {
+static bool rows_launch(const Q4RowsParams& p, bool append, cudaStream_t stream) {
   constexpr int kTokens = kRowThreads / (D / 8);
   const dim3 g((unsigned)(((int64_t)p.T + kTokens - 1) / kTokens), (unsigned)((p.H_kv + HEADS - 1) / HEADS));
-  if (append) kv_append_q4_kernel<D, HEADS><<<g, kRowThreads, 0, stream>>>(p);
-  else kv_read_q4_kernel<D, HEADS><<<g, kRowThreads, 0, stream>>>(p);
+  return append ? launch_dependent(kv_append_q4_kernel<D, HEADS>, g, kRowThreads, 0, p, stream)
+                : launch_dependent(kv_read_q4_kernel<D, HEADS>, g, kRowThreads, 0, p, stream);
 }
 
 int launch_q4_rows(const Q4RowsCall& c, bool append) {
@@ -174,9 +178,11 @@ int launch_q4_rows(const Q4RowsCall& c, bool append) {
   // Several heads per thread share its place in the cache; a call that could not fill
   // the GPU so is latency-bound and takes a head per thread.
   const bool many = (int64_t)c.T * c.H_kv * (c.D / 8) >= (int64_t)kQ4Heads * kRowThreads * kRowsFill;
-  if (c.D == 128) many ? rows_launch<128, kQ4Heads>(p, append, c.stream) : rows_launch<128, 1>(p, append, c.stream);
-  else many ? rows_launch<64, kQ4Heads>(p, append, c.stream) : rows_launch<64, 1>(p, append, c.stream);
-  return cudaGetLastError() == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA;
+  const bool ok =
+      c.D == 128
+          ? (many ? rows_launch<128, kQ4Heads>(p, append, c.stream) : rows_launch<128, 1>(p, append, c.stream))
+          : (many ? rows_launch<64, kQ4Heads>(p, append, c.stream) : rows_launch<64, 1>(p, append, c.stream));
+  return ok ? INKLING_OK : INKLING_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -207,6 +213,7 @@ constexpr int kExpandTokens = 16;  // tokens per block of the grid
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     q4_expand_kernel(const __grid_constant__ Q4ExpandParams p) {
+  await_previous_kernel();
   constexpr int U = D / 8;
   const int b = blockIdx.y;
   const int q_len = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
@@ -270,9 +277,9 @@ int launch_q4_expand(const Q4ExpandCall& c) {
   p.window = c.window;
   p.pages_per_seq = c.pages_per_seq;
   const dim3 grid((unsigned)(c.pages_per_seq * (64 / kExpandTokens)), (unsigned)c.B);
-  if (c.D == 128) q4_expand_kernel<128><<<grid, kRowThreads, 0, c.stream>>>(p);
-  else q4_expand_kernel<64><<<grid, kRowThreads, 0, c.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA;
+  const bool ok = c.D == 128 ? launch_dependent(q4_expand_kernel<128>, grid, kRowThreads, 0, p, c.stream)
+                             : launch_dependent(q4_expand_kernel<64>, grid, kRowThreads, 0, p, c.stream);
+  return ok ? INKLING_OK : INKLING_ERR_CUDA;
 }
 
 }  // namespace ira

@@ -15,14 +15,15 @@
 // makes the sums for itself; block 0 moves the pages, the others share the
 // slots.  One cluster barrier keeps the lengths, which may be updated in
 // place, from changing before every block has read them.  128 decoding requests
-// take 5.0 us (one block that went through the stack in memory: 7.9), 256 requests
-// with 16384 slots 6.8 us (17.8).
+// take 4.5 us (one block that went through the stack in memory: 7.9), 256 requests
+// with 16384 slots 6.4 us (17.8).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.h"
 #include "plan.cuh"
 #include "ptx.cuh"
 
@@ -90,6 +91,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
 
 __global__ void __launch_bounds__(kTabThreads)
     build_tables_kernel(const __grid_constant__ TablesParams p) {
+  await_previous_kernel();
   extern __shared__ int32_t sm[];
   int32_t* cu = sm;                // [B + 1] first token of each request
   int32_t* back = cu + p.B + 1;    // [B] rank of its first returned page
@@ -242,18 +244,9 @@ int launch_build_tables(const TablesCall& c) {
     return INKLING_ERR_CUDA;
   // one block for the pages, and one for every kTabThreads tokens, as many as a cluster may have
   const unsigned blocks = (unsigned)std::min(8, 1 + (int)(((int64_t)c.max_tokens + kTabThreads - 1) / kTabThreads));
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = blocks;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kTabThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p) == cudaSuccess ? INKLING_OK : INKLING_ERR_CUDA;
+  return launch_dependent(build_tables_kernel, dim3(blocks), kTabThreads, smem, p, c.stream, blocks)
+             ? INKLING_OK
+             : INKLING_ERR_CUDA;
 }
 
 }  // namespace ira
