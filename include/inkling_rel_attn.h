@@ -411,6 +411,8 @@ int inkling_rel_attn_kv_read_q4(
  *   Range: |q| <= 2^60, and V groups whose largest magnitude lies in 2^-37 ..
  * 2^57 (a group of smaller values is added with fewer bits, of larger ones may
  * overflow); K groups may use the cache's whole range.
+ *   page_table_stride * page_size times the items of a head (q_len tokens in groups
+ * of 8 / (H_q / H_kv), at least 1, by the heads in groups of 8) stays below 2^36.
  *   workspace  inkling_rel_attn_decode_q4_workspace_size bytes, 16-byte aligned,
  *              no content expected or kept; calls that may overlap need one each
  */

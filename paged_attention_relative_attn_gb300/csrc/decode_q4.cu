@@ -86,7 +86,8 @@ struct DecodeQ4Params {
   int B, pt_stride, H_q, H_kv, G, P, num_pages, R, window;
   int QL, TG;  // query tokens per sequence, per item
   int HI, HG;  // query heads of a KV head per item, items for all of them
-  int NG, NR;  // items per (sequence, KV head); rows of an item at most
+  int NT, NR;  // token groups of a sequence; rows of an item at most
+  int inv_G;   // 256 / G, rounded up (items of several tokens have all G <= 4 heads): rows divide by a product
   int slots;           // ring slots
   int bias_prefetch;   // rel_logits rows are 16-byte aligned
   float scale;         // of the products, which are 1 / kDown of <q, k>
@@ -98,7 +99,6 @@ struct Dq4Item {
   int tn, heads, pos0;
   int tile0, ntile;
   int part;  // -1: the whole item; else its part number of this thread block
-  int inv;   // 256 / heads, rounded up: rows (below 8) divide by a product
 };
 
 // What the producer prepares of an item, per lane of a consumer.
@@ -158,13 +158,13 @@ __device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Positions and tiles of item `grp` (token group, then head group) of a sequence of length L >= QL.
+// Positions and tiles of the items of token group tg of a sequence of length L >= QL.
 struct Dq4Range {
   int tn, pos0, tile0, ntile;
 };
-__device__ __forceinline__ Dq4Range group_range(const DecodeQ4Params& p, int L, int grp) {
+__device__ __forceinline__ Dq4Range group_range(const DecodeQ4Params& p, int L, int tg) {
   Dq4Range r;
-  const int first = grp / p.HG * p.TG;
+  const int first = tg * p.TG;
   r.tn = min(p.TG, p.QL - first);
   r.pos0 = L - p.QL + first;
   const int lo = p.window > 0 ? max(0, r.pos0 - p.window + 1) : 0;
@@ -180,8 +180,8 @@ __device__ __forceinline__ int head_tiles(const DecodeQ4Params& p, int b) {
   const int L = clamped_len(p, b);
   if (L < p.QL) return 0;
   int n = 0;
-  for (int g = 0; g < p.NG; ++g) n += group_range(p, L, g).ntile;
-  return n;
+  for (int tg = 0; tg < p.NT; ++tg) n += group_range(p, L, tg).ntile;
+  return n * p.HG;
 }
 
 // MULTI: items of several tokens, so rows of several positions.
@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
   auto item_at = [&](int s) { return smem + S.item_off + s * S.item_bytes; };
   auto item_rec = [&](int s) { return reinterpret_cast<Dq4Item*>(item_at(s)); };
   // token of an item's row r, and its packed row
-  auto token_of = [&](const Dq4Item& it, int r) { return MULTI ? (r * it.inv) >> 8 : 0; };
+  auto token_of = [&](int r) { return MULTI ? (r * p.inv_G) >> 8 : 0; };
   auto row_of = [&](const Dq4Item& it, int r) {
-    const int i = token_of(it, r);
+    const int i = token_of(r);
     return (size_t)it.row0 + (size_t)i * p.H_q + (r - i * it.heads);
   };
   // Key of a block that MMA row g (and g + 8: 8 more) stands for: rows 2t, 2t + 1
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       x1 = total * (blockIdx.x + 1) / runs;
     }
     // ---- the item at x
-    int b = 0, hkv = 0, grp = 0, nb = 0, off = 0, L = 0;  // nb: tiles per head of sequence b
+    int b = 0, hkv = 0, tg = 0, hg = 0, nb = 0, off = 0, L = 0;  // nb: tiles per head of sequence b
     if (x < x1) {
       int64_t carry = 0;
       for (int b0 = 0;; b0 += 32) {
@@ -288,7 +288,15 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
         carry += __shfl_sync(0xffffffffu, incl, 31);
       }
       L = clamped_len(p, b);
-      while (off >= group_range(p, L, grp).ntile) off -= group_range(p, L, grp++).ntile;
+      for (;;) {  // items of a head: token groups, head groups within them
+        const int n = group_range(p, L, tg).ntile;
+        if (off < n) break;
+        off -= n;
+        if (++hg == p.HG) {
+          hg = 0;
+          ++tg;
+        }
+      }
     }
 
     int ki = 0, kb = 0;  // items published, tiles sent
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = min(2 * t + x, rows - 1);
-        pr.pos[x] = it.pos0 + token_of(it, r);
+        pr.pos[x] = it.pos0 + token_of(r);
         const float* row = p.rel + row_of(it, r) * p.R;
         pr.bias[x] = row + (pr.pos[x] - key_g);
         pr.far[x] = it.pos0 + it.tn - 1 - TK * it.tile0 >= p.R ? __ldg(row + p.R - 1) : 0.f;
@@ -419,13 +427,12 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       return true;
     };
     while (x < x1 && ok) {
-      const Dq4Range r = group_range(p, L, grp);
+      const Dq4Range r = group_range(p, L, tg);
       Dq4Item it;
-      const int h0 = grp % p.HG * p.HI;  // its first head of the KV head's
-      it.row0 = (b * p.QL + grp / p.HG * p.TG) * p.H_q + hkv * p.G + h0;
+      const int h0 = hg * p.HI;  // its first head of the KV head's
+      it.row0 = (b * p.QL + tg * p.TG) * p.H_q + hkv * p.G + h0;
       it.tn = r.tn;
       it.heads = min(p.HI, p.G - h0);
-      it.inv = 255 / it.heads + 1;
       it.pos0 = r.pos0;
       it.tile0 = r.tile0 + off;
       it.ntile = (int)min((int64_t)(r.ntile - off), x1 - x);
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
         }
       }
       if (!copier && p.bias_prefetch && lane < it.tn * it.heads) {  // this row's bias for the part's keys
-        const int pr = it.pos0 + token_of(it, lane);
+        const int pr = it.pos0 + token_of(lane);
         const int far = pr - TK * it.tile0, near = pr - (TK * (it.tile0 + it.ntile) - 1);
         const int dlo = min(max(near, 0), p.R - 1) & ~3;
         const int dhi = min(min(max(far, 0), p.R - 1) + 4, p.R) & ~3;
@@ -532,8 +539,12 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       // ---- the next item
       x += it.ntile;
       off = 0;
-      if (++grp == p.NG) {
-        grp = 0;
+      if (++hg == p.HG) {
+        hg = 0;
+        ++tg;
+      }
+      if (tg == p.NT) {
+        tg = 0;
         if (++hkv == p.H_kv) {
           hkv = 0;
           do {
@@ -968,14 +979,14 @@ __global__ void __launch_bounds__(32 * kDq4MergeWarps) merge_q4_kernel(const __g
 // Host side
 
 struct Dq4Plan {
-  int G, TG, HI, HG, NG, NR, grid;
+  int G, TG, HI, HG, NT, NR, grid;
   size_t ml, cut, total;  // workspace offsets: parts first
   Dq4Plan(int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms) {
     G = H_q / H_kv;
     HG = (G + kDq4Rows - 1) / kDq4Rows;
     HI = (G + HG - 1) / HG;
     TG = std::min(QL, std::max(1, kDq4Rows / G));
-    NG = (QL + TG - 1) / TG * HG;
+    NT = (QL + TG - 1) / TG;
     NR = TG * HI;
     grid = sms * kDq4Ctas;
     ml = align256((size_t)grid * 2 * NR * D * sizeof(float));
@@ -1008,6 +1019,8 @@ static int launch_decode_q4_t(const DecodeQ4Call& c, DecodeQ4Params prm, const D
 
 int launch_decode_q4(const DecodeQ4Call& c) {
   const Dq4Plan plan(c.QL, c.H_q, c.H_kv, c.D, c.sms);
+  // a head's tiles, over all its items, are counted in 32 bits
+  if (((int64_t)c.pt_stride * c.P / kDq4Tile + 2) * plan.NT * plan.HG > INT32_MAX) return INKLING_ERR_ARG;
   DecodeQ4Params p;
   memset(&p, 0, sizeof(p));
   char* ws = static_cast<char*>(c.workspace);
@@ -1036,7 +1049,8 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   p.TG = plan.TG;
   p.HI = plan.HI;
   p.HG = plan.HG;
-  p.NG = plan.NG;
+  p.NT = plan.NT;
+  p.inv_G = 255 / plan.G + 1;
   p.NR = plan.NR;
   p.bias_prefetch = c.R % 4 == 0 && (reinterpret_cast<uintptr_t>(c.rel) & 15) == 0;
   p.scale = c.scale * kDown;
