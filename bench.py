@@ -851,6 +851,7 @@ KERNEL_SOURCES = {
     "prefill_kernel": ["paged_attention_relative_attn_gb300/csrc/prefill.cu",
                        "paged_attention_relative_attn_gb300/csrc/plan.cuh",
                        "paged_attention_relative_attn_gb300/csrc/ptx.cuh",
+                       "paged_attention_relative_attn_gb300/csrc/async.cuh",
                        "paged_attention_relative_attn_gb300/csrc/tc.cuh"],
 }
 

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libinkling_rel_attn.so")
 SOURCES = ["api.cu", "decode.cu", "decode_noalloc.cu", "prefill.cu", "selftest.cu", "kv_append.cu",
            "kv_conv.cu", "api_q4.cu", "q4_rows.cu", "decode_q4.cu", "tables.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "launch.h", "tc.cuh", "plan.cuh", "q4.cuh"]
+HEADERS = ["ptx.cuh", "async.cuh", "internal.h", "launch.h", "tc.cuh", "plan.cuh", "q4.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",

@@ -52,6 +52,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "async.cuh"
 #include "internal.h"
 #include "launch.h"
 #include "plan.cuh"

@@ -26,28 +26,12 @@ __device__ __forceinline__ unsigned long long globaltimer() {
   return t;
 }
 
-// For kernels launched with launch_dependent: nothing of the previous kernel's is
-// read or overwritten before the wait is over; the next one may be set up from now on.
-__device__ __forceinline__ void await_previous_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 __device__ __forceinline__ void fence_mbar_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-// All threads of all blocks of the cluster arrive, then wait; reads before the one
-// are done before writes after the other.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar)
@@ -112,49 +96,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
       }
       if (__shfl_sync(0xffffffffu, stop, 0)) return false;
     }
-  }
-}
-// mbarrier waits that let the hardware suspend the warp (up to kSuspendNs)
-// until the phase completes, instead of polling.
-constexpr uint32_t kSuspendNs = 20000;
-__device__ __forceinline__ bool mbar_try_wait_s(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kSuspendNs)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait_s(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
-  for (;;) {
-    if (mbar_try_wait_s(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer() - t0 > kWaitTimeoutNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool waitw(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait_s(bar, parity))) return true;
-  const unsigned long long t0 = globaltimer();
-  const bool leader = (threadIdx.x & 31) == 0;
-  for (;;) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_s(bar, parity))) return true;
-    int stop = 0;
-    if (leader) {
-      if (*abort) {
-        stop = 1;
-      } else if (globaltimer() - t0 > kWaitTimeoutNs) {
-        *abort = 1;
-        stop = 1;
-      }
-    }
-    if (__shfl_sync(0xffffffffu, stop, 0)) return false;
   }
 }
 // Bounded wait that ignores the abort flag (used to drain copies in flight).
@@ -281,32 +222,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Packed fp32 pairs (two lanes of one 64-bit register, .x in the low half):
-// fma / add / mul on both halves in one instruction, rounding as two scalar ones.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 }  // namespace ira

@@ -22,6 +22,7 @@
 
 #include <algorithm>
 
+#include "async.cuh"
 #include "internal.h"
 #include "launch.h"
 #include "plan.cuh"

@@ -332,6 +332,11 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     pass them to avoid allocations.  kv_lens=seq_lens and free_left=free_count
     step the state in place.  max_tokens is slot_map's length when that is given.
     """
+    if stream is not None:  # buffers made here are that stream's
+        with torch.cuda.stream(stream):
+            return build_tables(seq_lens, new_lens, page_table, free_pages, free_count, page_size=page_size,
+                                max_tokens=max_tokens, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, slot_map=slot_map,
+                                free_left=free_left, device_error=device_error)
     B = seq_lens.shape[0]
     if kv_lens is None:
         kv_lens = torch.empty_like(seq_lens)
@@ -360,7 +365,7 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
                       (free_count, "free_count", _I32, 1), (kv_lens, "kv_lens", _I32, 1),
                       (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (slot_map, "slot_map", _I64, 1),
                       (free_left, "free_left", _I32, 1)))
-    _launch("inkling_rel_attn_build_tables", dev, stream,
+    _launch("inkling_rel_attn_build_tables", dev, None,
             seq_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             free_pages.data_ptr(), free_count.data_ptr(), B, page_size, free_pages.shape[0],
             slot_map.shape[0], kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), slot_map.data_ptr(),
@@ -394,6 +399,9 @@ def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_e
     """Rows of the 4-bit cache as the bf16 values they stand for.  See
     inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
     """
+    if stream is not None:  # buffers made here are that stream's
+        with torch.cuda.stream(stream):
+            return kv_read_q4(slot_map, k_cache, v_cache, k_rows=k_rows, v_rows=v_rows, device_error=device_error)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
     T = slot_map.shape[0]
     if k_rows is None:
@@ -407,7 +415,7 @@ def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_e
             and k_rows.shape == v_rows.shape == (T, H_kv, D) and slot_map.dim() == 1):
         _refuse(dev, ((k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4), (slot_map, "slot_map", _I64, 1),
                       (k_rows, "k_rows", _BF16, 3), (v_rows, "v_rows", _BF16, 3)))
-    _launch("inkling_rel_attn_kv_read_q4", dev, stream,
+    _launch("inkling_rel_attn_kv_read_q4", dev, None,
             slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H_kv, D, P, n,
             k_rows.data_ptr(), v_rows.data_ptr(), _error_word(device_error, dev))
     return k_rows, v_rows
@@ -428,6 +436,10 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
     lse fp32 [B * q_len, H_q]).  Pass ``out``, ``lse`` and ``workspace``
     (decode_q4_workspace_bytes) to avoid allocations.
     """
+    if stream is not None:  # buffers made here are that stream's
+        with torch.cuda.stream(stream):
+            return decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len=q_len, window=window,
+                             scale=scale, out=out, lse=lse, workspace=workspace, device_error=device_error)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -449,7 +461,7 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
                       (page_table, "page_table", _I32, 2), (seq_lens, "seq_lens", _I32, 1),
                       (rel_logits, "rel_logits", _F32, 3), (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
     workspace, ws_bytes = _workspace(workspace, lambda: decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), q)
-    _launch("inkling_rel_attn_decode_q4", dev, stream,
+    _launch("inkling_rel_attn_decode_q4", dev, None,
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, rel_logits.shape[2],
             window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
@@ -471,6 +483,11 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
     Pass ``out``, ``lse`` and ``workspace`` (prefill_q4_workspace_bytes) to avoid
     allocations.
     """
+    if stream is not None:  # buffers made here are that stream's
+        with torch.cuda.stream(stream):
+            return prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window=window,
+                              scale=scale, max_seq_len=max_seq_len, max_q_len=max_q_len, out=out, lse=lse,
+                              workspace=workspace, device_error=device_error)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -495,7 +512,7 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
                       (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
     workspace, ws_bytes = _workspace(
         workspace, lambda: prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len), q)
-    _launch("inkling_rel_attn_prefill_q4", dev, stream,
+    _launch("inkling_rel_attn_prefill_q4", dev, None,
             q.data_ptr(), cu_seqlens_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
             max_q_len, H_q, H_kv, D, P, n, rel_logits.shape[2], window, scale, max_seq_len, out.data_ptr(),

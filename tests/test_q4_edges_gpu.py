@@ -116,3 +116,28 @@ def test_pages_go_from_ended_requests_to_several_others(ops):
     assert np.array_equal(d[3].cpu().numpy(), want["free"]) and int(left) == want["left"] and int(err) == 0
     live = slots[slots >= 0]
     assert live.unique().numel() == live.numel()
+
+
+def test_buffers_made_for_another_stream(ops):
+    """A freed tensor of the current stream, which still has a write to it in its queue, is not taken for the
+    buffers of a call on another stream."""
+    inp = make([1] * 3, [200, 77, 300], 4, 2, 128, 16, 0, 64, seed=95)
+    want, lwant = run_decode(ops, inp, 1)
+    slots = torch.arange(40, device=DEV)
+    kw, vw = ops.kv_read_q4(slots, inp.k_cache, inp.v_cache)
+    pf = dict(window=0, scale=inp.scale, max_seq_len=300, max_q_len=1)
+    cu = torch.arange(4, dtype=torch.int32, device=DEV)
+    args = (inp.k_cache, inp.v_cache, inp.page_table, inp.seq_lens, inp.rel_logits)
+    pwant, _ = ops.prefill_q4(inp.q, cu, *args, **pf)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: run_decode(ops, inp, 1, stream=side)[0], want),
+                      (lambda: run_decode(ops, inp, 1, stream=side)[1], lwant),
+                      (lambda: ops.kv_read_q4(slots, inp.k_cache, inp.v_cache, stream=side)[1], vw),
+                      (lambda: ops.prefill_q4(inp.q, cu, *args, stream=side, **pf)[0], pwant)):
+        torch.cuda._sleep(20_000_000)
+        old = [torch.zeros_like(ref) for _ in range(8)]      # written after the sleep
+        del old
+        got = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
