@@ -460,6 +460,21 @@ size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len,
                                                   int32_t max_seq_len);
 
 /*
+ * inkling_rel_attn_packed -- one of the calls on the 4-bit cache and the tables,
+ * with its `count` arguments in an array of 64-bit words, in the call's order:
+ * pointers and integers as they are, `scale` as the bits of a double, the stream
+ * last.  For bindings in which converting two dozen arguments one by one takes as
+ * long as the call.  An integer that does not fit its argument, a wrong count or
+ * an unknown call: INKLING_ERR_ARG.
+ */
+#define INKLING_PACKED_BUILD_TABLES 0
+#define INKLING_PACKED_KV_APPEND_Q4 1
+#define INKLING_PACKED_KV_READ_Q4 2
+#define INKLING_PACKED_DECODE_Q4 3
+#define INKLING_PACKED_PREFILL_Q4 4
+int inkling_rel_attn_packed(int32_t call, const int64_t* args, int32_t count);
+
+/*
  * inkling_rel_attn_choose_splits -- the decode split count, a pure host
  * function of host scalars (so it is identical at graph capture and replay,
  * and independent of physical page ids).  vLLM PR #51560, "Changes": the

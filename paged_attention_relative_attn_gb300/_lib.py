@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libinkling_rel_attn.so")
@@ -30,6 +31,7 @@ EXPORTED = (
     "inkling_rel_attn_decode_q4_workspace_size",
     "inkling_rel_attn_prefill_q4",
     "inkling_rel_attn_prefill_q4_workspace_size",
+    "inkling_rel_attn_packed",
     "inkling_rel_attn_choose_splits",
     "inkling_rel_attn_decode_workspace_size",
     "inkling_rel_attn_prefill_workspace_size",
@@ -98,6 +100,7 @@ _SIGS = {
         _i32, _i32, _i32, _f32, _i32,               # num_pages R window scale max_seq_len
         _p, _p, _p, _sz, _p, _p]),                  # out lse ws ws_bytes err stream
     "inkling_rel_attn_prefill_q4_workspace_size": (_sz, [_i32] * 6),
+    "inkling_rel_attn_packed": (ctypes.c_int, [_i32, ctypes.c_char_p, _i32]),  # call args count
     "inkling_rel_attn_choose_splits": (_i32, [_i32, _i32, _i32, _i32, _i32]),
     "inkling_rel_attn_decode_workspace_size": (_sz, [_i32] * 8),
     "inkling_rel_attn_prefill_workspace_size": (_sz, [_i32] * 3),
@@ -126,6 +129,22 @@ def load():
 
 def _v(x):
     return None if x in (None, 0) else int(x)
+
+
+# the calls of inkling_rel_attn_packed: number, packer of their words, count
+_q = struct.Struct
+PACKED = {
+    "inkling_rel_attn_build_tables": (0, _q("16q").pack, 16),
+    "inkling_rel_attn_kv_append_q4": (1, _q("12q").pack, 12),
+    "inkling_rel_attn_kv_read_q4": (2, _q("12q").pack, 12),
+    "inkling_rel_attn_decode_q4": (3, _q("16qd6q").pack, 23),
+    "inkling_rel_attn_prefill_q4": (4, _q("18qd7q").pack, 26),
+}
+
+
+def inkling_rel_attn_packed(call, args, count):
+    """``args``: the call's words as bytes (see PACKED)."""
+    return load().inkling_rel_attn_packed(call, args, count)
 
 
 def inkling_rel_attn_decode(q, k_cache, v_cache, page_table, page_table_stride, seq_lens,

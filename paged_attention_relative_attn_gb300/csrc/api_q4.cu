@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "internal.h"
 
@@ -259,6 +260,103 @@ int inkling_rel_attn_prefill_q4(const void* q, const int32_t* cu_seqlens_q, cons
   c.stream = static_cast<cudaStream_t>(stream);
   c.after_expansion = true;
   return launch_prefill(c);
+}
+
+int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
+  if (!a) return INKLING_ERR_ARG;
+  int at = 0;
+  bool fits = true;
+  auto ptr = [&]() { return reinterpret_cast<void*>(a[at++]); };
+  auto i32 = [&]() {
+    const int64_t v = a[at++];
+    fits = fits && v >= INT32_MIN && v <= INT32_MAX;
+    return (int32_t)v;
+  };
+  auto real = [&]() {
+    double v;
+    std::memcpy(&v, a + at++, sizeof(v));
+    return (float)v;
+  };
+  auto ci = [&]() { return static_cast<const int32_t*>(ptr()); };
+  // (braces: arguments are taken in order)
+  switch (call) {
+    case INKLING_PACKED_BUILD_TABLES: {
+      if (count != 16) return INKLING_ERR_ARG;
+      const int32_t *seq_lens = ci(), *new_lens = ci();
+      int32_t* table = static_cast<int32_t*>(ptr());
+      const int32_t stride = i32();
+      int32_t* free_pages = static_cast<int32_t*>(ptr());
+      const int32_t* free_count = ci();
+      const int32_t B = i32(), page_size = i32(), num_pages = i32(), max_tokens = i32();
+      int32_t* kv_lens = static_cast<int32_t*>(ptr());
+      int32_t* cu = static_cast<int32_t*>(ptr());
+      int64_t* slots = static_cast<int64_t*>(ptr());
+      int32_t* left = static_cast<int32_t*>(ptr());
+      int32_t* err = static_cast<int32_t*>(ptr());
+      void* stream = ptr();
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_build_tables(seq_lens, new_lens, table, stride, free_pages, free_count, B, page_size,
+                                           num_pages, max_tokens, kv_lens, cu, slots, left, err, stream);
+    }
+    case INKLING_PACKED_KV_APPEND_Q4:
+    case INKLING_PACKED_KV_READ_Q4: {
+      if (count != 12) return INKLING_ERR_ARG;
+      void *x = ptr(), *y = ptr(), *z = ptr();
+      const int32_t T = i32(), H_kv = i32(), D = i32(), page_size = i32(), num_pages = i32();
+      void *u = ptr(), *w = ptr();
+      int32_t* err = static_cast<int32_t*>(ptr());
+      void* stream = ptr();
+      if (!fits) return INKLING_ERR_ARG;
+      if (call == INKLING_PACKED_KV_APPEND_Q4)
+        return inkling_rel_attn_kv_append_q4(x, y, static_cast<const int64_t*>(z), T, H_kv, D, page_size, num_pages, u,
+                                             w, err, stream);
+      return inkling_rel_attn_kv_read_q4(static_cast<const int64_t*>(x), y, z, T, H_kv, D, page_size, num_pages, u, w,
+                                         err, stream);
+    }
+    case INKLING_PACKED_DECODE_Q4: {
+      if (count != 23) return INKLING_ERR_ARG;
+      const void *q = ptr(), *k = ptr(), *v = ptr();
+      const int32_t* table = ci();
+      const int32_t stride = i32();
+      const int32_t* seq_lens = ci();
+      const float* rel = static_cast<const float*>(ptr());
+      const int32_t B = i32(), q_len = i32(), H_q = i32(), H_kv = i32(), D = i32(), page_size = i32(),
+                    num_pages = i32(), R = i32(), window = i32();
+      const float scale = real();
+      void* out = ptr();
+      float* lse = static_cast<float*>(ptr());
+      void* ws = ptr();
+      const size_t ws_bytes = (size_t)a[at++];
+      int32_t* err = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_decode_q4(q, k, v, table, stride, seq_lens, rel, B, q_len, H_q, H_kv, D, page_size,
+                                        num_pages, R, window, scale, out, lse, ws, ws_bytes, err, ptr());
+    }
+    case INKLING_PACKED_PREFILL_Q4: {
+      if (count != 26) return INKLING_ERR_ARG;
+      const void* q = ptr();
+      const int32_t* cu = ci();
+      const void *k = ptr(), *v = ptr();
+      const int32_t* table = ci();
+      const int32_t stride = i32();
+      const int32_t* seq_lens = ci();
+      const float* rel = static_cast<const float*>(ptr());
+      const int32_t B = i32(), T = i32(), max_q_len = i32(), H_q = i32(), H_kv = i32(), D = i32(),
+                    page_size = i32(), num_pages = i32(), R = i32(), window = i32();
+      const float scale = real();
+      const int32_t max_seq_len = i32();
+      void* out = ptr();
+      float* lse = static_cast<float*>(ptr());
+      void* ws = ptr();
+      const size_t ws_bytes = (size_t)a[at++];
+      int32_t* err = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_prefill_q4(q, cu, k, v, table, stride, seq_lens, rel, B, T, max_q_len, H_q, H_kv, D,
+                                         page_size, num_pages, R, window, scale, max_seq_len, out, lse, ws, ws_bytes,
+                                         err, ptr());
+    }
+  }
+  return INKLING_ERR_ARG;
 }
 
 }  // extern "C"

@@ -274,15 +274,17 @@ def _refuse(dev, specs):
 
 
 def _launch(name, dev, stream, *args):
-    """One call into the C ABI on device ``dev`` (made current for it) and the given or current stream."""
+    """One call into the C ABI on device ``dev`` (made current for it) and the given or current stream, its
+    arguments packed (converting them one by one takes longer than the rest of the call)."""
     if dev < 0:
         raise ValueError(f"{name}: needs CUDA tensors")
-    fn = getattr(_lib.load(), name)
+    call, pack, count = _lib.PACKED[name]
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch._C._cuda_getDevice():
-        rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+        rc = _lib.load().inkling_rel_attn_packed(call, pack(*args, handle), count)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+            rc = _lib.load().inkling_rel_attn_packed(call, pack(*args, handle), count)
     if rc != 0:
         raise InklingError(rc, name)
 
@@ -290,7 +292,7 @@ def _launch(name, dev, stream, *args):
 def _error_word(device_error, dev):
     """Address of the optional error word."""
     if device_error is None:
-        return None
+        return 0
     if device_error.dtype is not _I32 or device_error.get_device() != dev or device_error.dim() != 1:
         raise TypeError("device_error: expected one int32 on the other tensors' device")
     return device_error.data_ptr()
