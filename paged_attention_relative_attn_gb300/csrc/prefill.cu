@@ -511,6 +511,8 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     }();
 
     float m_use = -INFINITY, l_part = 0.f;  // this half's running max (natural units) and sum
+    float nmu = 0.f;                        // -m_use log2 e
+    bool big = false;                       // m_use is so large that the rounding of nmu counts
     bool ok = true;
     int k = 0;
     for (; !cur.done(); ++k) {
@@ -588,16 +590,14 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
         const float r2 = fmax3(r11[6], r11[7], r11[8]), r3 = fmaxf(r11[9], r11[10]);
         mx = fmax3(r0, r1, fmaxf(r2, r3));
       }
-      float m_new = m_use, alpha = 1.f;
+      float alpha = 1.f;
       bool resc = false;
-      if (mx > -INFINITY) {
-        if (m_use == -INFINITY) {
-          m_new = mx;  // first visible keys of this row in my half: my O row is still zero
-        } else if (mx > m_use + kRescaleThreshold * kLn2) {
-          m_new = mx;
-          alpha = ex2((m_use - mx) * kLog2e);
-          resc = true;
-        }
+      if (mx > m_use + kRescaleThreshold * kLn2) {
+        resc = m_use > -INFINITY;  // (else the first visible keys of this row in my half: my O row is still zero)
+        if (resc) alpha = ex2((m_use - mx) * kLog2e);
+        m_use = mx;
+        nmu = -mx * kLog2e;
+        big = fabsf(mx) > kBigScore;
       }
       if (__any_sync(0xffffffffu, resc)) {
         // my O holds PV_0..PV_{k-1}; wait for the last one, then rescale it
@@ -616,26 +616,21 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
           tmem_st32(o_mine + 32 * cc, o);
         }
         tmem_st_wait();
+        l_part *= alpha;
       }
-      m_use = m_new;
-      l_part *= alpha;
-      const float nmu = (m_use == -INFINITY) ? 0.f : -m_use * kLog2e;
       uint32_t pk[16];
       // 2^(s log2 e - m log2 e) in one fma, or, where m is so large that the
       // rounding of m log2 e counts (masks such as -1e9 or fp32's lowest value
       // on every key so far), from the difference s - m
-      if (__any_sync(0xffffffffu, fabsf(m_use) > kBigScore && m_use > -INFINITY)) {
+      float sub = nmu;
+      if (__any_sync(0xffffffffu, big)) {
         const float base = m_use == -INFINITY ? 0.f : m_use;
-        float u = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          const float p0 = ex2((s[2 * m] - base) * kLog2e), p1 = ex2((s[2 * m + 1] - base) * kLog2e);
-          u += p0 + p1;
-          pk[m] = pack_bf16(p0, p1);
-        }
-        l_part += u;
-      } else {
-        const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), nmu2 = f2_pack(nmu, nmu);
+        for (int cc = 0; cc < 32; ++cc) s[cc] -= base;
+        sub = 0.f;
+      }
+      {
+        const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), nmu2 = f2_pack(sub, sub);
         uint64_t acc[4] = {0, 0, 0, 0};  // four packed partial sums (+0.0 bits)
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
