@@ -302,7 +302,7 @@ def _workspace(workspace, need, q):
     """(workspace, bytes): the given one, or a new one of ``need()`` bytes."""
     if workspace is None:
         workspace = torch.empty(need(), dtype=_U8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous and on the device of q")
     return workspace, workspace.nbytes
 
@@ -339,7 +339,7 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
             return build_tables(seq_lens, new_lens, page_table, free_pages, free_count, page_size=page_size,
                                 max_tokens=max_tokens, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, slot_map=slot_map,
                                 free_left=free_left, device_error=device_error)
-    B = seq_lens.shape[0]
+    B = seq_lens.numel()
     if kv_lens is None:
         kv_lens = torch.empty_like(seq_lens)
     if cu_seqlens_q is None:
@@ -384,7 +384,7 @@ def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None,
     uint8.
     """
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
-    T = slot_map.shape[0]
+    T = slot_map.numel()
     dev = k_new.get_device()
     if not (k_new.dtype is v_new.dtype is _BF16 and slot_map.dtype is _I64
             and v_new.get_device() == slot_map.get_device() == k_cache.get_device() == v_cache.get_device() == dev
@@ -405,7 +405,7 @@ def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_e
         with torch.cuda.stream(stream):
             return kv_read_q4(slot_map, k_cache, v_cache, k_rows=k_rows, v_rows=v_rows, device_error=device_error)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
-    T = slot_map.shape[0]
+    T = slot_map.numel()
     if k_rows is None:
         k_rows = torch.empty((T, H_kv, D), dtype=_BF16, device=k_cache.device)
     if v_rows is None:
@@ -442,13 +442,16 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
         with torch.cuda.stream(stream):
             return decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len=q_len, window=window,
                              scale=scale, out=out, lse=lse, workspace=workspace, device_error=device_error)
+    try:
+        (T, H_q, _), (rel_T, rel_H, R), (rows, stride), (B,) = (q.shape, rel_logits.shape, page_table.shape,
+                                                                seq_lens.shape)
+    except ValueError:  # one of another rank: refused below
+        T = H_q = rel_T = rel_H = R = rows = stride = B = -1
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
-    T, H_q = q.shape[:2]
-    B = seq_lens.shape[0]
     dev = q.get_device()
     if not (q.dtype is out.dtype is _BF16 and page_table.dtype is seq_lens.dtype is _I32
             and rel_logits.dtype is lse.dtype is _F32
@@ -456,16 +459,15 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
             == rel_logits.get_device() == out.get_device() == lse.get_device() == dev
             and q.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
             and rel_logits.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
-            and q.shape == out.shape == (B * q_len, H_q, D) and lse.shape == (T, H_q) and seq_lens.dim() == 1
-            and rel_logits.dim() == 3 and rel_logits.shape[:2] == (T, H_q)
-            and page_table.dim() == 2 and page_table.shape[0] == B):
+            and q.shape == out.shape == (B * q_len, H_q, D) and lse.shape == (T, H_q)
+            and rel_T == T and rel_H == H_q and rows == B):
         _refuse(dev, ((q, "q", _BF16, 3), (k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4),
                       (page_table, "page_table", _I32, 2), (seq_lens, "seq_lens", _I32, 1),
                       (rel_logits, "rel_logits", _F32, 3), (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
     workspace, ws_bytes = _workspace(workspace, lambda: decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), q)
     _launch("inkling_rel_attn_decode_q4", dev, None,
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
-            seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, rel_logits.shape[2],
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), stride,
+            seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, R,
             window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
             _error_word(device_error, dev))
     return out, lse
@@ -490,13 +492,16 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
             return prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window=window,
                               scale=scale, max_seq_len=max_seq_len, max_q_len=max_q_len, out=out, lse=lse,
                               workspace=workspace, device_error=device_error)
+    try:
+        (T, H_q, _), (rel_T, rel_H, R), (rows, stride), (B,) = (q.shape, rel_logits.shape, page_table.shape,
+                                                                seq_lens.shape)
+    except ValueError:  # one of another rank: refused below
+        T = H_q = rel_T = rel_H = R = rows = stride = B = -1
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
-    T, H_q = q.shape[:2]
-    B = seq_lens.shape[0]
     dev = q.get_device()
     if not (q.dtype is out.dtype is _BF16
             and page_table.dtype is seq_lens.dtype is cu_seqlens_q.dtype is _I32
@@ -506,8 +511,7 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
             and q.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
             and cu_seqlens_q.is_contiguous() and rel_logits.is_contiguous() and out.is_contiguous()
             and lse.is_contiguous() and q.shape == out.shape == (T, H_q, D) and lse.shape == (T, H_q)
-            and seq_lens.dim() == 1 and cu_seqlens_q.shape == (B + 1,) and rel_logits.dim() == 3
-            and rel_logits.shape[:2] == (T, H_q) and page_table.dim() == 2 and page_table.shape[0] == B):
+            and cu_seqlens_q.shape == (B + 1,) and rel_T == T and rel_H == H_q and rows == B >= 0):
         _refuse(dev, ((q, "q", _BF16, 3), (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (k_cache, "k_cache", _U8, 4),
                       (v_cache, "v_cache", _U8, 4), (page_table, "page_table", _I32, 2),
                       (seq_lens, "seq_lens", _I32, 1), (rel_logits, "rel_logits", _F32, 3),
@@ -516,8 +520,8 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
         workspace, lambda: prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len), q)
     _launch("inkling_rel_attn_prefill_q4", dev, None,
             q.data_ptr(), cu_seqlens_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
-            max_q_len, H_q, H_kv, D, P, n, rel_logits.shape[2], window, scale, max_seq_len, out.data_ptr(),
+            page_table.data_ptr(), stride, seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
+            max_q_len, H_q, H_kv, D, P, n, R, window, scale, max_seq_len, out.data_ptr(),
             lse.data_ptr(), workspace.data_ptr(), ws_bytes, _error_word(device_error, dev))
     return out, lse
 
