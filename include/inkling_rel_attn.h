@@ -319,6 +319,12 @@ int inkling_rel_attn_kv_conv_append(
  * cannot hold it (INKLING_DEVERR_SEQ_TOO_LONG; it takes no pages): its length
  * and row stay as they were and its new tokens get slot -1, so its outputs
  * of this step are to be ignored and it can ask again.
+ *   Its rows stay in the packing, so a call that places tokens by length
+ * (inkling_rel_attn_kv_append, inkling_rel_attn_kv_conv_append) must not be given
+ * kv_lens after a refusal: the unchanged length would put the refused rows over
+ * the last tokens that the request holds.  inkling_rel_attn_build_tables_step has
+ * the lengths for such calls.  inkling_rel_attn_kv_append_q4 goes by slot and
+ * needs none.
  *
  *   seq_lens      int32 [B], tokens held;  new_lens int32 [B]
  *   page_table    int32 [B, page_table_stride], rows of served requests extended
@@ -348,6 +354,24 @@ int inkling_rel_attn_build_tables(
     int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
     int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
     int32_t* free_left, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_build_tables_step -- inkling_rel_attn_build_tables with one
+ * more output, the lengths of the step:
+ *
+ *   step_lens     int32 [B], out: kv_lens, but 0 for a refused request.  NULL:
+ *                 not written.  A buffer of its own (not seq_lens or kv_lens)
+ * Given as seq_lens to the step's other calls they keep a refused request out of
+ * it: a sequence with fewer tokens than its rows is skipped by kv_append,
+ * kv_conv_append (its convolution state too), prefill and prefill_q4
+ * (INKLING_DEVERR_BAD_CHUNK), and gets out = 0, lse = -inf from the decode calls.
+ */
+int inkling_rel_attn_build_tables_step(
+    const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_table,
+    int32_t page_table_stride, int32_t* free_pages, const int32_t* free_count,
+    int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
+    int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
+    int32_t* free_left, int32_t* step_lens, int32_t* device_error, void* stream);
 
 /*
  * The 4-bit cache
@@ -463,7 +487,7 @@ size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len,
  * inkling_rel_attn_packed -- one of the calls on the 4-bit cache and the tables,
  * with its `count` arguments in an array of 64-bit words, in the call's order:
  * pointers and integers as they are, `scale` as the bits of a double, the stream
- * last.  For bindings in which converting two dozen arguments one by one takes as
+ * last (INKLING_PACKED_BUILD_TABLES: 16 words, or the 17 of the _step form).  For bindings in which converting two dozen arguments one by one takes as
  * long as the call.  An integer that does not fit its argument, a wrong count or
  * an unknown call: INKLING_ERR_ARG.
  */

@@ -25,6 +25,7 @@ EXPORTED = (
     "inkling_rel_attn_kv_append",
     "inkling_rel_attn_kv_conv_append",
     "inkling_rel_attn_build_tables",
+    "inkling_rel_attn_build_tables_step",
     "inkling_rel_attn_kv_append_q4",
     "inkling_rel_attn_kv_read_q4",
     "inkling_rel_attn_decode_q4",
@@ -82,6 +83,10 @@ _SIGS = {
         _p, _p, _p, _i32, _p, _p,                   # seq_lens new_lens page_table stride free count
         _i32, _i32, _i32, _i32,                     # B page_size num_pages max_tokens
         _p, _p, _p, _p, _p, _p]),                   # kv_lens cu slot_map free_left err stream
+    "inkling_rel_attn_build_tables_step": (ctypes.c_int, [
+        _p, _p, _p, _i32, _p, _p,                   # seq_lens new_lens page_table stride free count
+        _i32, _i32, _i32, _i32,                     # B page_size num_pages max_tokens
+        _p, _p, _p, _p, _p, _p, _p]),               # kv_lens cu slot_map free_left step_lens err stream
     "inkling_rel_attn_kv_append_q4": (ctypes.c_int, [
         _p, _p, _p, _i32, _i32, _i32, _i32, _i32,   # k_new v_new slot_map T H_kv D page_size num_pages
         _p, _p, _p, _p]),                           # k_cache v_cache err stream
@@ -135,6 +140,7 @@ def _v(x):
 _q = struct.Struct
 PACKED = {
     "inkling_rel_attn_build_tables": (0, _q("16q").pack, 16),
+    "inkling_rel_attn_build_tables_step": (0, _q("17q").pack, 17),
     "inkling_rel_attn_kv_append_q4": (1, _q("12q").pack, 12),
     "inkling_rel_attn_kv_read_q4": (2, _q("12q").pack, 12),
     "inkling_rel_attn_decode_q4": (3, _q("16qd6q").pack, 23),
@@ -226,6 +232,15 @@ def inkling_rel_attn_build_tables(seq_lens, new_lens, page_table, page_table_str
         _v(seq_lens), _v(new_lens), _v(page_table), page_table_stride, _v(free_pages),
         _v(free_count), B, page_size, num_pages, max_tokens, _v(kv_lens), _v(cu_seqlens_q),
         _v(slot_map), _v(free_left), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_build_tables_step(seq_lens, new_lens, page_table, page_table_stride, free_pages,
+                                       free_count, B, page_size, num_pages, max_tokens, kv_lens,
+                                       cu_seqlens_q, slot_map, free_left, step_lens, device_error, stream):
+    return load().inkling_rel_attn_build_tables_step(
+        _v(seq_lens), _v(new_lens), _v(page_table), page_table_stride, _v(free_pages),
+        _v(free_count), B, page_size, num_pages, max_tokens, _v(kv_lens), _v(cu_seqlens_q),
+        _v(slot_map), _v(free_left), _v(step_lens), _v(device_error), _v(stream))
 
 
 def inkling_rel_attn_kv_append_q4(k_new, v_new, slot_map, T, H_kv, D, page_size, num_pages, k_cache,

@@ -75,6 +75,16 @@ int inkling_rel_attn_build_tables(const int32_t* seq_lens, const int32_t* new_le
                                   int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
                                   int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
                                   int32_t* free_left, int32_t* device_error, void* stream) {
+  return inkling_rel_attn_build_tables_step(seq_lens, new_lens, page_table, page_table_stride, free_pages, free_count,
+                                            B, page_size, num_pages, max_tokens, kv_lens, cu_seqlens_q, slot_map,
+                                            free_left, nullptr, device_error, stream);
+}
+
+int inkling_rel_attn_build_tables_step(const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_table,
+                                       int32_t page_table_stride, int32_t* free_pages, const int32_t* free_count,
+                                       int32_t B, int32_t page_size, int32_t num_pages, int32_t max_tokens,
+                                       int32_t* kv_lens, int32_t* cu_seqlens_q, int64_t* slot_map,
+                                       int32_t* free_left, int32_t* step_lens, int32_t* device_error, void* stream) {
   if (B < 0 || B > kTablesMaxBatch || max_tokens < 0 || max_tokens == INT32_MAX) return INKLING_ERR_ARG;
   if (page_size <= 0 || page_size % 16 != 0 || page_size > 256) return INKLING_ERR_ARG;
   if (num_pages <= 0 || num_pages == INT32_MAX || page_table_stride <= 0) return INKLING_ERR_ARG;
@@ -85,7 +95,7 @@ int inkling_rel_attn_build_tables(const int32_t* seq_lens, const int32_t* new_le
     return INKLING_ERR_ARG;
   if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(page_table, 4) || !aligned(free_pages, 4) ||
       !aligned(free_count, 4) || !aligned(kv_lens, 4) || !aligned(cu_seqlens_q, 4) || !aligned(slot_map, 8) ||
-      !aligned(free_left, 4) || !aligned(device_error, 4))
+      !aligned(free_left, 4) || !aligned(step_lens, 4) || !aligned(device_error, 4))
     return INKLING_ERR_ALIGN;
   if (device_info().ok != 1) return INKLING_ERR_DEVICE;
   TablesCall c;
@@ -103,6 +113,7 @@ int inkling_rel_attn_build_tables(const int32_t* seq_lens, const int32_t* new_le
   c.cu_seqlens_q = cu_seqlens_q;
   c.slot_map = slot_map;
   c.free_left = free_left;
+  c.step_lens = step_lens;
   c.dev_err = device_error;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_build_tables(c);
@@ -281,7 +292,7 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
   // (braces: arguments are taken in order)
   switch (call) {
     case INKLING_PACKED_BUILD_TABLES: {
-      if (count != 16) return INKLING_ERR_ARG;
+      if (count != 16 && count != 17) return INKLING_ERR_ARG;
       const int32_t *seq_lens = ci(), *new_lens = ci();
       int32_t* table = static_cast<int32_t*>(ptr());
       const int32_t stride = i32();
@@ -292,11 +303,12 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
       int32_t* cu = static_cast<int32_t*>(ptr());
       int64_t* slots = static_cast<int64_t*>(ptr());
       int32_t* left = static_cast<int32_t*>(ptr());
+      int32_t* step = count == 17 ? static_cast<int32_t*>(ptr()) : nullptr;
       int32_t* err = static_cast<int32_t*>(ptr());
       void* stream = ptr();
       if (!fits) return INKLING_ERR_ARG;
-      return inkling_rel_attn_build_tables(seq_lens, new_lens, table, stride, free_pages, free_count, B, page_size,
-                                           num_pages, max_tokens, kv_lens, cu, slots, left, err, stream);
+      return inkling_rel_attn_build_tables_step(seq_lens, new_lens, table, stride, free_pages, free_count, B, page_size,
+                                                num_pages, max_tokens, kv_lens, cu, slots, left, step, err, stream);
     }
     case INKLING_PACKED_KV_APPEND_Q4:
     case INKLING_PACKED_KV_READ_Q4: {

@@ -173,6 +173,7 @@ struct TablesCall {
   int32_t* cu_seqlens_q;
   int64_t* slot_map;
   int32_t* free_left;
+  int32_t* step_lens;  // or null
   int32_t* dev_err;
   cudaStream_t stream;
 };

@@ -42,6 +42,7 @@ struct TablesParams {
   int32_t* cu;
   int64_t* slot_map;
   int32_t* free_left;
+  int32_t* step_lens;
   int32_t* dev_err;
   uint64_t inv_P;  // 2^64 / P rounded up: lengths divide by the high half of a product
   int B, pt_stride, P, num_pages, max_tokens;
@@ -211,7 +212,10 @@ __global__ void __launch_bounds__(kTabThreads)
   for (int b = tid; b < p.B; b += kTabThreads) {
     const int n_in = p.new_lens[b];
     const int L_in = p.seq_lens[b];
-    p.kv_lens[b] = n_in < 0 ? 0 : first[b] >= 0 ? L_in + n_in : L_in;
+    const bool served = first[b] >= 0;  // ended requests too
+    const int after = n_in < 0 ? 0 : served ? L_in + n_in : L_in;
+    p.kv_lens[b] = after;
+    if (p.step_lens) p.step_lens[b] = served ? after : 0;
     p.cu[b] = cu[b];
   }
   if (tid == 0) {
@@ -231,6 +235,7 @@ int launch_build_tables(const TablesCall& c) {
   p.cu = c.cu_seqlens_q;
   p.slot_map = c.slot_map;
   p.free_left = c.free_left;
+  p.step_lens = c.step_lens;
   p.dev_err = c.dev_err;
   p.B = c.B;
   p.pt_stride = c.pt_stride;

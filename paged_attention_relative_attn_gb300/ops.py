@@ -322,8 +322,8 @@ def _q4_cache(k_cache, v_cache):
 
 
 def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page_size, max_tokens=None,
-                 kv_lens=None, cu_seqlens_q=None, slot_map=None, free_left=None, device_error=None,
-                 stream=None):
+                 kv_lens=None, cu_seqlens_q=None, slot_map=None, free_left=None, step_lens=None,
+                 device_error=None, stream=None):
     """The tables of one serving step, from request lengths.  See
     inkling_rel_attn_build_tables.
 
@@ -333,12 +333,15 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     cu_seqlens_q [B + 1] int32, slot_map [max_tokens] int64, free_left [1] int32);
     pass them to avoid allocations.  kv_lens=seq_lens and free_left=free_count
     step the state in place.  max_tokens is slot_map's length when that is given.
+    step_lens [B] int32, if given, is written too: kv_lens, but 0 for a refused
+    request.  Calls that place tokens by length (kv_append, kv_conv_append) take it
+    instead of kv_lens, which would put refused rows over a request's last tokens.
     """
     if stream is not None:  # buffers made here are that stream's
         with torch.cuda.stream(stream):
             return build_tables(seq_lens, new_lens, page_table, free_pages, free_count, page_size=page_size,
                                 max_tokens=max_tokens, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, slot_map=slot_map,
-                                free_left=free_left, device_error=device_error)
+                                free_left=free_left, step_lens=step_lens, device_error=device_error)
     B = seq_lens.numel()
     if kv_lens is None:
         kv_lens = torch.empty_like(seq_lens)
@@ -367,11 +370,14 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
                       (free_count, "free_count", _I32, 1), (kv_lens, "kv_lens", _I32, 1),
                       (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (slot_map, "slot_map", _I64, 1),
                       (free_left, "free_left", _I32, 1)))
-    _launch("inkling_rel_attn_build_tables", dev, None,
+    if step_lens is not None and not (step_lens.dtype is _I32 and step_lens.get_device() == dev
+                                      and step_lens.is_contiguous() and step_lens.shape == seq_lens.shape):
+        _refuse(dev, ((step_lens, "step_lens", _I32, 1),))
+    _launch("inkling_rel_attn_build_tables_step", dev, None,
             seq_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             free_pages.data_ptr(), free_count.data_ptr(), B, page_size, free_pages.shape[0],
             slot_map.shape[0], kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), slot_map.data_ptr(),
-            free_left.data_ptr(), _error_word(device_error, dev))
+            free_left.data_ptr(), 0 if step_lens is None else step_lens.data_ptr(), _error_word(device_error, dev))
     return kv_lens, cu_seqlens_q, slot_map, free_left
 
 
