@@ -316,7 +316,9 @@ int inkling_rel_attn_kv_conv_append(
  * then pages are taken from the top, in batch order.  A request needing pages
  * is served iff the pages asked for by it and by all requests before it are
  * there; otherwise it is refused (INKLING_DEVERR_NO_PAGES), as is one whose row
- * cannot hold it (INKLING_DEVERR_SEQ_TOO_LONG; it takes no pages): its length
+ * cannot hold it (INKLING_DEVERR_SEQ_TOO_LONG; it takes no pages) and one with new
+ * tokens that are not all among the first max_tokens of the packing, which have the
+ * slots (INKLING_DEVERR_BAD_CHUNK; it takes no pages): its length
  * and row stay as they were and its new tokens get slot -1, so its outputs
  * of this step are to be ignored and it can ask again.
  *   Its rows stay in the packing, so a call that places tokens by length
@@ -344,8 +346,9 @@ int inkling_rel_attn_kv_conv_append(
  * free_count it steps the state in place, in a captured graph too.  Page ids
  * outside [0, num_pages) on the stack set INKLING_DEVERR_BAD_PAGE and give slot
  * -1, and so does a stack that would grow past num_pages (the pages past it are
- * dropped); more new tokens than max_tokens set INKLING_DEVERR_BAD_CHUNK (the
- * tokens past it get no slot).  B <= 8192 (0: nothing is written), page_size as
+ * dropped).  Prefix sums stop at 2^31 - 1: a batch that asks for that many tokens
+ * has no packing, sets INKLING_DEVERR_BAD_CHUNK, and max_tokens refuses nobody in
+ * it (tokens past it get no slot).  B <= 8192 (0: nothing is written), page_size as
  * everywhere, num_pages and max_tokens below 2^31 - 1.
  */
 int inkling_rel_attn_build_tables(

@@ -126,9 +126,13 @@ def ref_build_tables(seq_lens, new_lens, page_table, free_pages, free_count, P, 
         if n < 0:
             continue
         had, need = -(-L // P), -(-(L + n) // P) - (-(-L // P))
+        if n > 0 and cu[-1] > max_tokens:
+            bits.add("bad_chunk")
         if L + n > stride * P:
             bits.add("too_long")
             need, served = 0, False
+        elif n > 0 and cu[-1] > max_tokens:
+            served = False
         else:
             asked += need
             served = need == 0 or asked <= top
@@ -141,8 +145,6 @@ def ref_build_tables(seq_lens, new_lens, page_table, free_pages, free_count, P, 
         kv[b] = L + n if served else L
         for p in range(L, L + n):
             slots.append(int(table[b, p // P]) * P + p % P if served else -1)
-    if len(slots) > max_tokens:
-        bits.add("bad_chunk")
     slots = (slots + [-1] * max_tokens)[:max_tokens]
     return dict(kv_lens=kv, cu=np.array(cu), slots=np.array(slots, dtype=np.int64), table=table, free=free,
                 left=left, bits=bits)

@@ -140,16 +140,19 @@ __global__ void __launch_bounds__(kTabThreads)
   const int F = min(max(count, 0), p.num_pages);
   const int top = (int)min((uint32_t)F + all.gone, (uint32_t)p.num_pages);  // the stack once pages have come back
   int used = 0;
+  const bool packed = all.n < 0x7fffffffu;  // else offsets have stopped, and the slot map's length decides nothing
   for (int b = b0; b < b1; ++b) {
     const Ask a = ask_of(p, p.seq_lens[b], p.new_lens[b]);
-    const bool served = !a.bad && (a.need == 0 || at.need + a.need <= (uint32_t)top);
+    const bool room = !packed || a.n == 0 || at.n + a.n <= (uint32_t)p.max_tokens;  // a slot for each of its tokens
+    // (requests after one without room have none either, so pages taken still are a prefix of those asked for)
+    const bool served = !a.bad && room && (a.need == 0 || at.need + a.need <= (uint32_t)top);
     cu[b] = (int)at.n;
     back[b] = (int)at.gone;
     first[b] = served ? (int)min(at.need, (uint32_t)top) : -1;
     lens[b] = a.L;
     if (mover) {
       if (a.bad) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
-      else if (!served) report(p.dev_err, INKLING_DEVERR_NO_PAGES);
+      else if (room && !served) report(p.dev_err, INKLING_DEVERR_NO_PAGES);
     }
     at = at + Sum3{(uint32_t)a.n, a.gone, a.need};
     if (served && a.need > 0) used = (int)at.need;  // served requests that take pages are a prefix
