@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kTabThreads)
   if (tid == 0) {
     cu[p.B] = (int)all.n;
     if (mover && all.n > (uint32_t)p.max_tokens) report(p.dev_err, INKLING_DEVERR_BAD_CHUNK);
-    else if (mover && (uint32_t)F + all.gone > (uint32_t)p.num_pages) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+    if (mover && (uint32_t)F + all.gone > (uint32_t)p.num_pages) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
   }
   __syncthreads();
   cluster_arrive();  // this block has read the lengths
