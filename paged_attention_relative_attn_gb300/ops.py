@@ -333,6 +333,7 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     cu_seqlens_q [B + 1] int32, slot_map [max_tokens] int64, free_left [1] int32);
     pass them to avoid allocations.  kv_lens=seq_lens and free_left=free_count
     step the state in place.  max_tokens is slot_map's length when that is given.
+    Without requests: no tokens, no slot (-1), the stack as it is.
     step_lens [B] int32, if given, is written too: kv_lens, but 0 for a refused
     request.  Calls that place tokens by length (kv_append, kv_conv_append) take it
     instead of kv_lens, which would put refused rows over a request's last tokens.
@@ -378,6 +379,11 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
             free_pages.data_ptr(), free_count.data_ptr(), B, page_size, free_pages.shape[0],
             slot_map.shape[0], kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), slot_map.data_ptr(),
             free_left.data_ptr(), 0 if step_lens is None else step_lens.data_ptr(), _error_word(device_error, dev))
+    if B == 0:  # nothing was launched: an empty packing, no slot, the stack as it is
+        cu_seqlens_q.zero_()
+        slot_map.fill_(-1)
+        if free_left.data_ptr() != free_count.data_ptr():
+            free_left.copy_(free_count)
     return kv_lens, cu_seqlens_q, slot_map, free_left
 
 
