@@ -465,10 +465,13 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       // two lanes share one) at a time.  A lane's copies go out as soon as its slot is
       // free; page ids are read a batch ahead.
       const int32_t* pt_row = p.page_table + (size_t)b * p.pt_stride;
-      const int pos1 = it.pos0 + it.tn - 1;
-      auto page_of = [&](int i, int u) -> int {  // page of block u of tile i; -1: past the last key
+      // Blocks of a tile that no row sees, past the last key or before the window, are not
+      // looked up: their pages may be gone.  (Only the first tile has some before the window.)
+      const int pos1 = it.pos0 + it.tn - 1, klo = p.window > 0 ? max(0, it.pos0 - p.window + 1) : 0;
+      auto seen = [&](int key) { return key <= pos1 && key + 15 >= klo; };
+      auto page_of = [&](int i, int u) -> int {  // page of block u of tile i; -1: not seen
         const int key = (it.tile0 + i) * TK + 16 * u;
-        return copier && lane < batch && i < it.ntile && (u == 0 || key <= pos1) ? __ldg(pt_row + key / p.P) : -1;
+        return copier && lane < batch && i < it.ntile && seen(key) ? __ldg(pt_row + key / p.P) : -1;
       };
       int page[U], next[U];
 #pragma unroll
@@ -508,9 +511,9 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               live += fine[u] ? 1 : 0;
-              // a bad page reads as zeros: scale 0 (16 * N bf16 of K and of V); past the last
-              // key nothing is needed
-              if (!fine[u] && (u == 0 || key0 + 16 * u <= pos1)) {
+              // a bad page reads as zeros: scale 0 (16 * N bf16 of K and of V); of a block that
+              // no row sees nothing is needed
+              if (!fine[u] && seen(key0 + 16 * u)) {
 #pragma unroll 1
                 for (int w = 0; w < 8 * N; ++w) {
                   reinterpret_cast<uint32_t*>(dst + u * BLK + q4_scale_off(D))[w] = 0u;
