@@ -431,7 +431,8 @@ int inkling_rel_attn_kv_read_q4(
  * decode.  Same formula on the values x * s, same shapes, lengths and errors;
  * one more rule: a row all of whose visible scores are -inf gets out = 0, lse =
  * -inf.  Keys past a row's position or window, and places past a sequence's
- * end, may hold any bytes.
+ * end, may hold any bytes; page ids of pages wholly before every row's window are
+ * not looked at.
  *   The work is cut over the GPU by the batch's lengths, read on the device:
  * no host bound on them is needed, and results do not depend on page ids or
  * timing (they do depend, in the last bits, on the other lengths in the batch).

@@ -73,6 +73,7 @@ constexpr int kDq4Threads = 32 * (kDq4W + 2);
 constexpr int kDq4MergeWarps = 4;     // of the joining kernel's blocks: a thread per channel in all
 constexpr int kDq4U = 2;              // 16-token blocks per tile
 constexpr int kDq4Tile = 16 * kDq4U;  // keys per tile
+static_assert(kDq4U == 2, "a tile's first and last block");
 constexpr int kDq4Rows = 8;           // rows of an item at most: the N of an MMA
 
 struct DecodeQ4Params {
@@ -465,13 +466,16 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
       // two lanes share one) at a time.  A lane's copies go out as soon as its slot is
       // free; page ids are read a batch ahead.
       const int32_t* pt_row = p.page_table + (size_t)b * p.pt_stride;
-      // Blocks of a tile that no row sees, past the last key or before the window, are not
-      // looked up: their pages may be gone.  (Only the first tile has some before the window.)
-      const int pos1 = it.pos0 + it.tn - 1, klo = p.window > 0 ? max(0, it.pos0 - p.window + 1) : 0;
-      auto seen = [&](int key) { return key <= pos1 && key + 15 >= klo; };
+      // Blocks of a tile that no row sees are not looked up: their pages may be gone.  A
+      // tile has a key that is seen, so its first block can lie before the window only, and
+      // its last past the last key only.  (Where pages hold whole tiles the first block's is
+      // the last one's, and both come in one copy.)
+      const int pos1 = it.pos0 + it.tn - 1;
+      const int before = (p.window > 0 && p.P % TK != 0 ? max(0, it.pos0 - p.window + 1) : 0) - 15;
+      auto seen = [&](int key, int u) { return u == 0 ? key >= before : key <= pos1; };
       auto page_of = [&](int i, int u) -> int {  // page of block u of tile i; -1: not seen
         const int key = (it.tile0 + i) * TK + 16 * u;
-        return copier && lane < batch && i < it.ntile && seen(key) ? __ldg(pt_row + key / p.P) : -1;
+        return copier && lane < batch && i < it.ntile && seen(key, u) ? __ldg(pt_row + key / p.P) : -1;
       };
       int page[U], next[U];
 #pragma unroll
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kDq4Threads, kDq4Ctas)
               live += fine[u] ? 1 : 0;
               // a bad page reads as zeros: scale 0 (16 * N bf16 of K and of V); of a block that
               // no row sees nothing is needed
-              if (!fine[u] && seen(key0 + 16 * u)) {
+              if (!fine[u] && seen(key0 + 16 * u, u)) {
 #pragma unroll 1
                 for (int w = 0; w < 8 * N; ++w) {
                   reinterpret_cast<uint32_t*>(dst + u * BLK + q4_scale_off(D))[w] = 0u;
