@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreads)
       p.table_out[(size_t)b * p.pages_per_seq + i] = b * p.pages_per_seq + i;
   }
   const int j0 = base + (int)blockIdx.x * kExpandTokens;  // all in one 16-token block of the cache
-  if (!fits || j0 >= L) return;
+  if (!fits || j0 >= L || j0 + kExpandTokens <= lo) return;  // keys before lo are not attended to: their page may be gone
   const int lp = j0 / p.P;
   const int page = __ldg(p.page_table + (size_t)b * p.pt_stride + lp);
   const bool ok = page >= 0 && page < p.num_pages;

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from tests.q4_cases import check, make
-from tests.test_q4_gpu import DEV, run_decode
+from tests.test_q4_gpu import DEV, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,28 @@ def test_decode(ops, P, q_len, D, G):
     assert int(err) == 0
     assert torch.equal(out, want) and torch.equal(lse, lwant)
     check(inp, out, lse)
+
+
+@pytest.mark.parametrize("P", [16, 32, 48, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill(ops, P, D):
+    q_lens, lens = [1, 130, 7, 40, 3], [300, 500, 176, 161, 1000]
+    inp = make(q_lens, lens, 4, 2, D, P, 50, 64, seed=200 + P)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    need = ops.prefill_q4_workspace_bytes(len(lens), 130, 2, D, 50, 1000)
+    want, lwant = run_prefill(ops, inp)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # NaN in every bf16 of it
+    out, lse = run_prefill(ops, without_old_pages(inp, q_lens), workspace=ws, device_error=err)
+    assert int(err) == 0
+    assert torch.equal(out, want) and torch.equal(lse, lwant)
+    check(inp, out, lse)
+
+
+@pytest.mark.parametrize("P", [16, 64])
+def test_widest_window(ops, P):
+    """A window of 2^31 - 1 keys hides nothing."""
+    inp = make([2, 2, 2], [2, 40, 300], 4, 2, 64, P, 0, 64, seed=9)
+    wide = dataclasses.replace(inp, window=2 ** 31 - 1)
+    for call in (lambda x: run_decode(ops, x, 2), lambda x: run_prefill(ops, x)):
+        for a, b in zip(call(inp), call(wide)):
+            assert torch.equal(a, b)
