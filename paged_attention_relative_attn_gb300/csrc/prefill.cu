@@ -652,8 +652,12 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       if (t.dirty) {
         // rows outside [klo, khi] may hold other keys' values (NaN included):
         // zero them in V so that P = 0 times V stays 0 in the tensor core
-        const int st = k % kVStages;
-        if (!waitw(smem_u32(&v_full[st]), (k / kVStages) & 1, abort_flag)) {
+        // (this warp does not follow v_full otherwise, and may be here before V of the
+        // stage's previous tile has come in: the wait's parity would then be that of the
+        // tile before it.  So first that tile's PV, whose barrier moves with these warps.)
+        const int st = k % kVStages, kp = k - kVStages;
+        if ((kp >= 0 && !waitw(smem_u32(&pv_done[kp % kSBufs]), (kp / kSBufs) & 1, abort_flag)) ||
+            !waitw(smem_u32(&v_full[st]), (k / kVStages) & 1, abort_flag)) {
           ok = false;
           break;
         }
