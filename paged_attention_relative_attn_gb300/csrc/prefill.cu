@@ -622,12 +622,13 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       // 2^(s log2 e - m log2 e) in one fma, or, where m is so large that the
       // rounding of m log2 e counts (masks such as -1e9 or fp32's lowest value
       // on every key so far), from the difference s - m
+      // (row by row: the other rows of the warp subtract 0 and keep their bits)
       float sub = nmu;
       if (__any_sync(0xffffffffu, big)) {
-        const float base = m_use == -INFINITY ? 0.f : m_use;
+        const float base = big ? m_use : 0.f;
 #pragma unroll
         for (int cc = 0; cc < 32; ++cc) s[cc] -= base;
-        sub = 0.f;
+        sub = big ? 0.f : nmu;
       }
       {
         const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), nmu2 = f2_pack(sub, sub);
