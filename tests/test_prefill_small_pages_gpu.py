@@ -1,5 +1,5 @@
-"""Prefill over pages that are no multiple of 64 tokens, through many key tiles, the last of them partly visible: close
-to the oracle and the same bits in every run."""
+"""Prefill through many key tiles, the last of them partly visible inside its page, as pages of other than 64 tokens
+leave it: close to the oracle and the same bits in every run."""
 
 from __future__ import annotations
 
@@ -18,6 +18,9 @@ CASES = [
     ([1, 129, 300], [777, 1000, 300], 6, 2, 128, 32, 0, 64),
     ([200, 33, 5], [1000, 2000, 450], 4, 4, 64, 80, 700, 256),
     ([260], [3000], 8, 1, 128, 16, 1500, 1024),
+    ([140, 70], [410, 330], 2, 1, 128, 128, 0, 512),
+    ([100, 140, 1], [1800, 600, 1360], 4, 2, 64, 256, 0, 64),
+    ([130] * 3, [721, 980, 3000], 6, 1, 128, 192, 900, 512),
     ([64] * 12, [211 + 64 * i + i for i in range(12)], 16, 8, 128, 48, 0, 128),
 ]
 
