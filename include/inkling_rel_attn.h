@@ -436,9 +436,12 @@ int inkling_rel_attn_kv_read_q4(
  *   The work is cut over the GPU by the batch's lengths, read on the device:
  * no host bound on them is needed, and results do not depend on page ids or
  * timing (they do depend, in the last bits, on the other lengths in the batch).
- *   Range: |q| <= 2^60, and V groups whose largest magnitude lies in 2^-37 ..
- * 2^57 (a group of smaller values is added with fewer bits, of larger ones may
- * overflow); K groups may use the cache's whole range.
+ *   Range, narrower than the cache's: |q| <= 2^60, |scale| <= 2^54 (checked), and V
+ * groups whose largest magnitude lies in 2^-37 .. 2^57 (a group of smaller values is
+ * added with fewer bits, of larger ones may overflow).  K groups may use the cache's
+ * whole range; a score carries, beside fp32's rounding, an absolute error of up to
+ * 2^-60 |scale| max(k, 2^-9), k being the largest magnitude in K, which counts where
+ * q is below 2^-40 and K or the scale huge.
  *   page_table_stride * page_size times the items of a head (q_len tokens in groups
  * of 8 / (H_q / H_kv), at least 1, by the heads in groups of 8) stays below 2^36.
  *   workspace  inkling_rel_attn_decode_q4_workspace_size bytes, 16-byte aligned,

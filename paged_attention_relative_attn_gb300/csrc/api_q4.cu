@@ -153,7 +153,7 @@ int inkling_rel_attn_decode_q4(const void* q, const void* k_cache, const void* v
   if (!common_shape_ok(H_q, H_kv, D, page_size, num_pages, R, page_table_stride)) return INKLING_ERR_ARG;
   if ((int64_t)B * q_len * H_q > INT32_MAX / 4) return INKLING_ERR_ARG;
   if ((int64_t)num_pages * H_kv > INT32_MAX / (page_size / 16)) return INKLING_ERR_ARG;  // the pool's blocks
-  if (!(scale == scale)) return INKLING_ERR_ARG;
+  if (!(scale >= -0x1p54f && scale <= 0x1p54f)) return INKLING_ERR_ARG;  // times 2^73 it stays finite
   if (B == 0) return INKLING_OK;
   if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !rel_logits || !out) return INKLING_ERR_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
