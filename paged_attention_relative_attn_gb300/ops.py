@@ -289,6 +289,12 @@ def _launch(name, dev, stream, *args):
         raise InklingError(rc, name)
 
 
+def _own_stream(stream, t):
+    """A given stream has to be of the tensors' device (of another one's the call would not run on it)."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {t.device}")
+
+
 def _error_word(device_error, dev):
     """Address of the optional error word."""
     if device_error is None:
@@ -339,6 +345,7 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     instead of kv_lens, which would put refused rows over a request's last tokens.
     """
     if stream is not None:  # buffers made here are that stream's
+        _own_stream(stream, seq_lens)
         with torch.cuda.stream(stream):
             return build_tables(seq_lens, new_lens, page_table, free_pages, free_count, page_size=page_size,
                                 max_tokens=max_tokens, kv_lens=kv_lens, cu_seqlens_q=cu_seqlens_q, slot_map=slot_map,
@@ -395,6 +402,8 @@ def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None,
     negative: skipped); k_cache, v_cache [num_pages, H_kv, page_size, 9 * D / 16]
     uint8.
     """
+    if stream is not None:
+        _own_stream(stream, k_new)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
     T = slot_map.numel()
     dev = k_new.get_device()
@@ -414,6 +423,7 @@ def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_e
     inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
     """
     if stream is not None:  # buffers made here are that stream's
+        _own_stream(stream, k_cache)
         with torch.cuda.stream(stream):
             return kv_read_q4(slot_map, k_cache, v_cache, k_rows=k_rows, v_rows=v_rows, device_error=device_error)
     n, H_kv, P, D = _q4_cache(k_cache, v_cache)
@@ -451,6 +461,7 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
     (decode_q4_workspace_bytes) to avoid allocations.
     """
     if stream is not None:  # buffers made here are that stream's
+        _own_stream(stream, q)
         with torch.cuda.stream(stream):
             return decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len=q_len, window=window,
                              scale=scale, out=out, lse=lse, workspace=workspace, device_error=device_error)
@@ -500,6 +511,7 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
     allocations.
     """
     if stream is not None:  # buffers made here are that stream's
+        _own_stream(stream, q)
         with torch.cuda.stream(stream):
             return prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window=window,
                               scale=scale, max_seq_len=max_seq_len, max_q_len=max_q_len, out=out, lse=lse,
