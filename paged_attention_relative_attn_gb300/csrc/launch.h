@@ -1,7 +1,10 @@
 // Launches whose set-up overlaps the end of the kernel before them in the stream
 // (programmatic stream serialization).  The kernel waits for that one's completion
 // itself (await_previous_kernel), in all of its blocks and before anything else in
-// global memory; with a plain kernel before it nothing changes.
+// global memory; with a plain kernel before it nothing changes.  The kernel before may
+// still write while this one's blocks are there, so what it can have written (lengths,
+// tables, slots, rows, queries, biases) is not read through the read-only path
+// (__ldg, ld.global.nc), which is for memory that nobody writes during a kernel's life.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
 
   // ---- the sequence's scalars, loaded together; their latency overlaps the
   // barrier and TMEM set-up below, and nothing reads them before it
-  const int tb = __ldg(p.cu_seqlens_q + b);
-  const int te = __ldg(p.cu_seqlens_q + b + 1);
-  const int L_in = __ldg(p.seq_lens + b);
+  const int tb = p.cu_seqlens_q[b];
+  const int te = p.cu_seqlens_q[b + 1];
+  const int L_in = p.seq_lens[b];
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::BAR_OFF);
   uint64_t* q_full = bars;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       if (lp < batch_base || lp >= batch_base + 32) {
         batch_base = lp;
         const int idx = lp + lane;
-        my_page = (idx < p.pt_stride) ? __ldg(pt_row + idx) : 0;
+        my_page = (idx < p.pt_stride) ? pt_row[idx] : 0;
       }
       return __shfl_sync(0xffffffffu, my_page, lp - batch_base);
     };
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     const int pi = pos0 + i;         // its absolute position
     const int lo_i = p.window > 0 ? max(0, pi - p.window + 1) : 0;
     const size_t row_off = ((size_t)(valid ? t0 + i : t0) * p.H_q + h) * R;
-    const float clampv = valid ? __ldg(p.rel + row_off + R - 1) : 0.f;
+    const float clampv = valid ? p.rel[row_off + R - 1] : 0.f;
     const uint32_t tlane = tmem + ((uint32_t)(32 * lg) << 16);
     const uint32_t o_mine = tlane + kOCol + kOHalfStride * grp;
     const float scale = p.scale;

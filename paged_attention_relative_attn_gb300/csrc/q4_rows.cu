@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const int i = threadIdx.x % U, j = i >> 2, t = i & 3;
   uint4 kr[HEADS], vr[HEADS];
   int64_t slot = -1;
-  if (t_row < p.T) slot = __ldg(p.slots + t_row);
+  if (t_row < p.T) slot = p.slots[t_row];
 #pragma unroll
   for (int x = 0; x < HEADS; ++x) {
     kr[x] = vr[x] = make_uint4(0, 0, 0, 0);
@@ -112,10 +112,10 @@ __device__ __forceinline__ void q4_read8(const uint8_t* kb, const uint8_t* vb, b
   constexpr int N = D / kQ4Group;
   uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
   if (have) {
-    kw = __ldg(reinterpret_cast<const uint32_t*>(kb + r * (D / 2)) + N * t + j);
-    vw = __ldg(reinterpret_cast<const uint32_t*>(vb + r * (D / 2)) + v_word<D>(j, t));
-    ks = __ldg(reinterpret_cast<const uint16_t*>(kb + q4_scale_off(D)) + r * N + j);
-    vs = __ldg(reinterpret_cast<const uint16_t*>(vb + q4_scale_off(D)) + r * N + j);
+    kw = reinterpret_cast<const uint32_t*>(kb + r * (D / 2))[N * t + j];
+    vw = reinterpret_cast<const uint32_t*>(vb + r * (D / 2))[v_word<D>(j, t)];
+    ks = reinterpret_cast<const uint16_t*>(kb + q4_scale_off(D))[r * N + j];
+    vs = reinterpret_cast<const uint16_t*>(vb + q4_scale_off(D))[r * N + j];
   }
   k = q4_values8(kw, ks);
   v = q4_values8(v_swap(vw, j), vs);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int U = D / 8;
   const int t_row = blockIdx.x * (kRowThreads / U) + threadIdx.x / U, h0 = blockIdx.y * HEADS;
   const int i = threadIdx.x % U;
-  int64_t slot = t_row < p.T ? __ldg(p.slots + t_row) : -1;
+  int64_t slot = t_row < p.T ? p.slots[t_row] : -1;
   if (slot >= (int64_t)p.num_pages * p.P) {
     report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
     slot = -1;
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kRowThreads)
   await_previous_kernel();
   constexpr int U = D / 8;
   const int b = blockIdx.y;
-  const int q_len = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
-  const int L_in = __ldg(p.seq_lens + b);
+  const int q_len = p.cu[b + 1] - p.cu[b];
+  const int L_in = p.seq_lens[b];
   const int L = min(max(L_in, 0), p.pt_stride * p.P);
   const int lo = p.window > 0 ? max(0, L - q_len - p.window + 1) : 0;
   const int base = lo & ~63;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const int j0 = base + (int)blockIdx.x * kExpandTokens;  // all in one 16-token block of the cache
   if (!fits || j0 >= L || j0 + kExpandTokens <= lo) return;  // keys before lo are not attended to: their page may be gone
   const int lp = j0 / p.P;
-  const int page = __ldg(p.page_table + (size_t)b * p.pt_stride + lp);
+  const int page = p.page_table[(size_t)b * p.pt_stride + lp];
   const bool ok = page >= 0 && page < p.num_pages;
   if (!ok && threadIdx.x == 0) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
   // thread: 8 channels of one row, head after head (with D = 64 half of the block has every other head)
