@@ -15,12 +15,13 @@ __device__ __forceinline__ void await_previous_kernel() {
 }
 
 // All threads of all blocks of the cluster arrive, then wait; reads before the one
-// are done before writes after the other.
+// are done before writes after the other.  (Not .aligned: a warp's threads may come one by
+// one, as out of a loop with a trip count of each thread's own.)
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // mbarrier waits that let the hardware suspend the warp (up to kSuspendNs)
