@@ -91,7 +91,8 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTabThreads)
+// (1 block per SM: without it the compiler keeps to 32 registers and spills; 5.0 us instead of 4.55)
+__global__ void __launch_bounds__(kTabThreads, 1)
     build_tables_kernel(const __grid_constant__ TablesParams p) {
   await_previous_kernel();
   extern __shared__ int32_t sm[];
