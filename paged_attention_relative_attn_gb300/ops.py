@@ -299,7 +299,8 @@ def _error_word(device_error, dev):
     """Address of the optional error word."""
     if device_error is None:
         return 0
-    if device_error.dtype is not _I32 or device_error.get_device() != dev or device_error.dim() != 1:
+    if (device_error.dtype is not _I32 or device_error.get_device() != dev or device_error.dim() != 1
+            or device_error.numel() < 1):
         raise TypeError("device_error: expected one int32 on the other tensors' device")
     return device_error.data_ptr()
 
