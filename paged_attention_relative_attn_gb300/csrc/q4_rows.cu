@@ -26,7 +26,7 @@ namespace ira {
 
 constexpr int kRowThreads = 256;
 constexpr int kQ4Heads = 2;           // heads per thread of a large call (8192 tokens x 16 heads both ways: 30 us; 1: 33.7, 4: 31.9)
-constexpr int kRowsFill = 152 * 4;    // blocks that give every SM some
+constexpr int kRowsFill = 4;          // such blocks per SM from which on it is taken
 
 struct Q4RowsParams {
   uint4* k_rows;  // [T][H_kv][D / 8] of 8 x bf16
@@ -179,8 +179,10 @@ static bool rows_launch(const Q4RowsParams& p, bool append, cudaStream_t stream)
 int launch_q4_rows(const Q4RowsCall& c, bool append) {
   const Q4RowsParams p = rows_params(c);
   // Several heads per thread share its place in the cache; a call that could not fill
-  // the GPU so is latency-bound and takes a head per thread.
-  const bool many = (int64_t)c.T * c.H_kv * (c.D / 8) >= (int64_t)kQ4Heads * kRowThreads * kRowsFill;
+  // the GPU so is latency-bound and takes a head per thread.  Append and read, blocks at
+  // one head a thread, 152 SMs (border 1216): 128 blocks 3.07 us with one head and 3.65
+  // with two, 512: 4.2 and 4.5, 1024: 6.75 and 7.2, 2048: 10.7 and 10.7, 4096: 17.9 and 16.3.
+  const bool many = (int64_t)c.T * c.H_kv * (c.D / 8) >= (int64_t)kQ4Heads * kRowThreads * kRowsFill * sm_count();
   const bool ok =
       c.D == 128
           ? (many ? rows_launch<128, kQ4Heads>(p, append, c.stream) : rows_launch<128, 1>(p, append, c.stream))
