@@ -182,7 +182,7 @@ int launch_q4_rows(const Q4RowsCall& c, bool append) {
   // the GPU so is latency-bound and takes a head per thread.  Append and read, blocks at
   // one head a thread, 152 SMs (border 1216): 128 blocks 3.07 us with one head and 3.65
   // with two, 512: 4.2 and 4.5, 1024: 6.75 and 7.2, 2048: 10.7 and 10.7, 4096: 17.9 and 16.3.
-  const bool many = (int64_t)c.T * c.H_kv * (c.D / 8) >= (int64_t)kQ4Heads * kRowThreads * kRowsFill * sm_count();
+  const bool many = (int64_t)c.T * c.H_kv * (c.D / 8) >= (int64_t)kQ4Heads * kRowThreads * kRowsFill * device_info().sms;
   const bool ok =
       c.D == 128
           ? (many ? rows_launch<128, kQ4Heads>(p, append, c.stream) : rows_launch<128, 1>(p, append, c.stream))

@@ -166,3 +166,50 @@ def test_captured(ops):
         assert step.tolist() == want, i
     assert lens.tolist() == [18, 16]
     assert bool((kc[1, 15] == 2.0).all()) and bool((kc[3, 1] == 4.0).all())
+
+
+def test_too_few_slots_and_rows(ops):
+    """Refused for slots: the caller's rows end before the packing does, and the appends leave its cache alone."""
+    s = Step(ops, (3, 4, 2), max_tokens=5)  # rows 0..4: request 1's last two rows and request 2's are not there
+    assert s.kv.tolist() == [19, 16, 5] and s.step.tolist() == [19, 0, 0] and int(s.err) == 8
+    kc, vc = rows(PAGES, P, H, D, seed=3), rows(PAGES, P, H, D, seed=4)
+    wk, wv = kc.clone(), vc.clone()
+    k, v = s.k[:5].contiguous(), s.v[:5].contiguous()
+    ops.kv_append(k, v, s.cu, s.step, s.pt, kc, vc)
+    for t, slot in enumerate(s.slots.tolist()):
+        if slot >= 0:
+            wk[slot // P, slot % P], wv[slot // P, slot % P] = k[t], v[t]
+    assert torch.equal(kc, wk) and torch.equal(vc, wv) and s.slots.tolist().count(-1) == 2
+    width = 3
+    w = torch.randn((H, D, width), generator=torch.Generator().manual_seed(5)).to(DEV)
+    st = [rows(3, width - 1, H, D, seed=6 + i) for i in range(2)]
+    before = [x.clone() for x in st]
+    pools = [rows(PAGES, P, H, D, seed=8 + i) for i in range(2)]
+    old = [x.clone() for x in pools]
+    ops.kv_conv_append(k, v, s.cu, s.step, s.pt, pools[0], pools[1], w, w, st[0], st[1], i32([0, 1, 2]), max_q_len=4)
+    for x, y in zip(st, before):
+        assert torch.equal(x[1:], y[1:]) and not torch.equal(x[0], y[0])
+    for x, y in zip(pools, old):
+        assert torch.equal(x[[1, 2]], y[[1, 2]]) and not torch.equal(x[7], y[7])
+
+
+def test_convolved_rows_for_the_4_bit_cache(ops):
+    """The convolution into a staging pool, whose lengths are the step's new tokens and 0 for a refused request, then the
+    4-bit append by slot: the refused request keeps its state and its rows."""
+    new = (1, 14, 2)
+    s = Step(ops, new)
+    width = 4
+    w = torch.randn((H, D, width), generator=torch.Generator().manual_seed(5)).to(DEV)
+    st = [rows(3, width - 1, H, D, seed=6 + i) for i in range(2)]
+    before = [x.clone() for x in st]
+    stage = [torch.zeros((3, P, H, D), dtype=BF16, device=DEV) for _ in range(2)]
+    mine = torch.where(s.step > 0, i32(new), 0).to(torch.int32)
+    ops.kv_conv_append(s.k, s.v, s.cu, mine, i32([[0], [1], [2]]), stage[0], stage[1], w, w, st[0], st[1], i32([0, 1, 2]),
+                       max_q_len=14)
+    pool = torch.randint(0, 256, (PAGES, H, P, 9 * D // 16), dtype=torch.uint8, device=DEV)
+    kc, vc = pool.clone(), pool.clone()
+    at = torch.cat([torch.arange(n, device=DEV) + b * P for b, n in enumerate(new)])  # the rows' places in the staging pool
+    ops.kv_append_q4(stage[0].view(-1, H, D)[at], stage[1].view(-1, H, D)[at], s.slots, kc, vc)
+    for x, y in zip(st, before):
+        assert torch.equal(x[1], y[1]) and not torch.equal(x[0], y[0]) and not torch.equal(x[2], y[2])
+    assert torch.equal(kc[1], pool[1]) and torch.equal(vc[1], pool[1]) and not torch.equal(kc[7], pool[7])
