@@ -165,9 +165,9 @@ __device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32
 }
 
 // A plain load, not one of the read-only path (launch.h), that the compiler may still move
-// among the arithmetic around it (as an ordinary load, which stays in its place, drafts took 57.6 us instead of
-// 54.5).  Its address comes from shared memory written after the wait for the kernel
-// before, so it cannot move ahead of that.
+// among the arithmetic around it (as an ordinary load, which stays in its place, drafts
+// took 57.6 us instead of 54.5).  Its address comes from shared memory written after the
+// wait for the kernel before, so it cannot move ahead of that.
 __device__ __forceinline__ float load_bias(const float* at) {
   float v;
   asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
