@@ -493,7 +493,102 @@ size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len,
                                                   int32_t max_seq_len);
 
 /*
- * inkling_rel_attn_packed -- one of the calls on the 4-bit cache and the tables,
+ * The 8-bit cache
+ * ---------------
+ * The entry points named *_q8 work on K and V pools held in 8 bits with a scale for
+ * each block of 16 tokens and KV head, paged like the others: uint8
+ * [num_pages][H_kv][page_size * (D + 1)], 258 bytes per token and KV head for D =
+ * 128, K and V together.  Within one (page, KV head) tokens come in blocks of 16 (K
+ * and V each on its own): 16 rows of D e4m3 numbers, then the scale 2^e as fp32, 16
+ * bits that mark rows with a NaN (bit r: row r), and 10 zero bytes.
+ *   e     the smallest integer in -60 .. 55 with max |v| <= 448 * 2^e over the
+ *         block's rows; magnitudes above 448 * 2^55, infinities too, count as that
+ *   x     v / 2^e rounded to the nearest e4m3 number, ties to even
+ * and a place stands for x * 2^e -- always a bf16 number, so reading a row back
+ * rounds nothing.  A value is off by at most 2^-4 of itself, or 2^(e - 10) if that
+ * is more.  A row with a NaN holds zeros, does not count for e, and reads as NaN in
+ * all its channels.
+ *   Channel c of row r of a block is at byte
+ *     K, D = 128:  128 r + 16 (c / 16 ^ 4 (r % 2)) + c % 16       K, D = 64:  64 r + c
+ *     V, D = 128:  128 r + 16 (c / 16 ^ 2 (r / 2 % 4)) + c % 16
+ *     V, D = 64:   128 (r / 2) + 8 (4 (2 (r % 2) + c / 32 ^ r / 2 % 4) + c / 8 % 4) + c % 8
+ * (^: exclusive or; the rows that a matrix instruction takes side by side so lie in
+ * different banks of shared memory).  D in {64, 128}; pools 16-byte aligned, zeros
+ * before their first use.
+ */
+
+/*
+ * inkling_rel_attn_kv_append_q8 -- quantise the new tokens' K and V rows into
+ * the 8-bit cache; arguments and errors as for inkling_rel_attn_kv_append_q4.
+ *   A token at place 0 of a block (place % 16 == 0) begins it anew: what the block
+ * held is no longer valid.  Tokens at other places join it: where they need a larger
+ * e the block's other rows are rounded again from the values that they stand for
+ * (exact unless a value falls under 2^-6 of the new scale: e4m3 holds fewer bits
+ * there), and e does not fall when a row is overwritten, as after rejected drafts.
+ *   The tokens of one block must lie within 16 consecutive tokens of the call (slots of
+ * a request's tokens do; skipped and other tokens may lie between them) and have
+ * distinct slots; else the block holds a mixture.  Blocks of
+ * pages that two requests own (inkling_rel_attn_fork_pages) must not be appended to.
+ * Apart from the blocks that tokens go to no byte of the cache is written.
+ */
+int inkling_rel_attn_kv_append_q8(
+    const void* k_new, const void* v_new, const int64_t* slot_map, int32_t T,
+    int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    void* k_cache, void* v_cache, int32_t* device_error, void* stream);
+
+/* inkling_rel_attn_kv_read_q8 -- rows of the 8-bit cache as the bf16 values they
+ * stand for; arguments and errors as for inkling_rel_attn_kv_read_q4. */
+int inkling_rel_attn_kv_read_q8(
+    const int64_t* slot_map, const void* k_cache, const void* v_cache,
+    int32_t T, int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    void* k_rows, void* v_rows, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_decode_q8 -- inkling_rel_attn_decode_q4 over the 8-bit cache: the
+ * last q_len (1 .. 64) tokens of each sequence, on the values x * 2^e.  Keys past a
+ * row's position or window, and places past a sequence's end, may hold any bytes;
+ * the blocks that hold a visible key are as the append left them.
+ *   Range: q to 2^60, |scale| <= 2^54 (checked), |scale| times the largest |q| and |k|
+ * to 2^100 (q of a row and K of a block enter as numbers relative to their largest
+ * magnitude: what a q value loses lies below 2^-39 of its row's largest).  V blocks
+ * with a scale below 2^-20 of the largest among the keys that a thread block adds up are
+ * added with fewer bits: the error is at most 2^-32 of the largest weight times 448
+ * times the largest scale, for each key.
+ *   Workspace, bounds and errors as for inkling_rel_attn_decode_q4.
+ */
+int inkling_rel_attn_decode_q8(
+    const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* page_table, int32_t page_table_stride,
+    const int32_t* seq_lens, const float* rel_logits, int32_t B, int32_t q_len,
+    int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+    int32_t R, int32_t window, float scale, void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes, int32_t* device_error,
+    void* stream);
+
+/* Workspace bytes of inkling_rel_attn_decode_q8 for these scalars. */
+size_t inkling_rel_attn_decode_q8_workspace_size(int32_t B, int32_t q_len,
+                                                 int32_t H_q, int32_t H_kv,
+                                                 int32_t D, int32_t num_sms);
+
+/* inkling_rel_attn_prefill_q8 -- inkling_rel_attn_prefill_q4 over the 8-bit cache:
+ * the keys that a chunk sees are expanded into bf16 pages in the workspace, exactly. */
+int inkling_rel_attn_prefill_q8(
+    const void* q, const int32_t* cu_seqlens_q, const void* k_cache,
+    const void* v_cache, const int32_t* page_table, int32_t page_table_stride,
+    const int32_t* seq_lens, const float* rel_logits, int32_t B, int32_t T,
+    int32_t max_q_len, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+    int32_t num_pages, int32_t R, int32_t window, float scale,
+    int32_t max_seq_len, void* out, float* lse_out, void* workspace,
+    size_t workspace_bytes, int32_t* device_error, void* stream);
+
+/* Workspace bytes of inkling_rel_attn_prefill_q8 for these scalars.  Host only. */
+size_t inkling_rel_attn_prefill_q8_workspace_size(int32_t B, int32_t max_q_len,
+                                                  int32_t H_kv, int32_t D,
+                                                  int32_t window,
+                                                  int32_t max_seq_len);
+
+/*
+ * inkling_rel_attn_packed -- one of the calls on the 4-bit and 8-bit caches and the tables,
  * with its `count` arguments in an array of 64-bit words, in the call's order:
  * pointers and integers as they are, `scale` as the bits of a double, the stream
  * last (INKLING_PACKED_BUILD_TABLES: 16 words, or the 17 of the _step form).  For bindings in which converting two dozen arguments one by one takes as
@@ -505,6 +600,10 @@ size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len,
 #define INKLING_PACKED_KV_READ_Q4 2
 #define INKLING_PACKED_DECODE_Q4 3
 #define INKLING_PACKED_PREFILL_Q4 4
+#define INKLING_PACKED_KV_APPEND_Q8 5
+#define INKLING_PACKED_KV_READ_Q8 6
+#define INKLING_PACKED_DECODE_Q8 7
+#define INKLING_PACKED_PREFILL_Q8 8
 int inkling_rel_attn_packed(int32_t call, const int64_t* args, int32_t count);
 
 /*

@@ -32,6 +32,12 @@ EXPORTED = (
     "inkling_rel_attn_decode_q4_workspace_size",
     "inkling_rel_attn_prefill_q4",
     "inkling_rel_attn_prefill_q4_workspace_size",
+    "inkling_rel_attn_kv_append_q8",
+    "inkling_rel_attn_kv_read_q8",
+    "inkling_rel_attn_decode_q8",
+    "inkling_rel_attn_decode_q8_workspace_size",
+    "inkling_rel_attn_prefill_q8",
+    "inkling_rel_attn_prefill_q8_workspace_size",
     "inkling_rel_attn_packed",
     "inkling_rel_attn_choose_splits",
     "inkling_rel_attn_decode_workspace_size",
@@ -115,6 +121,13 @@ _SIGS = {
 }
 
 
+# the 8-bit cache's calls take what the 4-bit cache's do
+for _name in ("kv_append", "kv_read", "decode", "prefill"):
+    _SIGS[f"inkling_rel_attn_{_name}_q8"] = _SIGS[f"inkling_rel_attn_{_name}_q4"]
+for _name in ("decode", "prefill"):
+    _SIGS[f"inkling_rel_attn_{_name}_q8_workspace_size"] = _SIGS[f"inkling_rel_attn_{_name}_q4_workspace_size"]
+
+
 def load():
     """Load the shared library (once) and declare the C signatures."""
     global _lib
@@ -145,6 +158,10 @@ PACKED = {
     "inkling_rel_attn_kv_read_q4": (2, _q("12q").pack, 12),
     "inkling_rel_attn_decode_q4": (3, _q("16qd6q").pack, 23),
     "inkling_rel_attn_prefill_q4": (4, _q("18qd7q").pack, 26),
+    "inkling_rel_attn_kv_append_q8": (5, _q("12q").pack, 12),
+    "inkling_rel_attn_kv_read_q8": (6, _q("12q").pack, 12),
+    "inkling_rel_attn_decode_q8": (7, _q("16qd6q").pack, 23),
+    "inkling_rel_attn_prefill_q8": (8, _q("18qd7q").pack, 26),
 }
 
 
@@ -283,6 +300,49 @@ def inkling_rel_attn_prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, p
 
 def inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len):
     return load().inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window,
+                                                             max_seq_len)
+
+
+def inkling_rel_attn_kv_append_q8(k_new, v_new, slot_map, T, H_kv, D, page_size, num_pages, k_cache,
+                                  v_cache, device_error, stream):
+    return load().inkling_rel_attn_kv_append_q8(
+        _v(k_new), _v(v_new), _v(slot_map), T, H_kv, D, page_size, num_pages, _v(k_cache),
+        _v(v_cache), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_kv_read_q8(slot_map, k_cache, v_cache, T, H_kv, D, page_size, num_pages, k_rows,
+                                v_rows, device_error, stream):
+    return load().inkling_rel_attn_kv_read_q8(
+        _v(slot_map), _v(k_cache), _v(v_cache), T, H_kv, D, page_size, num_pages, _v(k_rows),
+        _v(v_rows), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_decode_q8(q, k_cache, v_cache, page_table, page_table_stride, seq_lens,
+                               rel_logits, B, q_len, H_q, H_kv, D, page_size, num_pages, R, window,
+                               scale, out, lse_out, workspace, workspace_bytes, device_error, stream):
+    return load().inkling_rel_attn_decode_q8(
+        _v(q), _v(k_cache), _v(v_cache), _v(page_table), page_table_stride, _v(seq_lens),
+        _v(rel_logits), B, q_len, H_q, H_kv, D, page_size, num_pages, R, window, scale, _v(out),
+        _v(lse_out), _v(workspace), workspace_bytes, _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_decode_q8_workspace_size(B, q_len, H_q, H_kv, D, num_sms):
+    return load().inkling_rel_attn_decode_q8_workspace_size(B, q_len, H_q, H_kv, D, num_sms)
+
+
+def inkling_rel_attn_prefill_q8(q, cu_seqlens_q, k_cache, v_cache, page_table, page_table_stride,
+                                seq_lens, rel_logits, B, T, max_q_len, H_q, H_kv, D, page_size,
+                                num_pages, R, window, scale, max_seq_len, out, lse_out, workspace,
+                                workspace_bytes, device_error, stream):
+    return load().inkling_rel_attn_prefill_q8(
+        _v(q), _v(cu_seqlens_q), _v(k_cache), _v(v_cache), _v(page_table), page_table_stride,
+        _v(seq_lens), _v(rel_logits), B, T, max_q_len, H_q, H_kv, D, page_size, num_pages, R,
+        window, scale, max_seq_len, _v(out), _v(lse_out), _v(workspace), workspace_bytes,
+        _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_prefill_q8_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len):
+    return load().inkling_rel_attn_prefill_q8_workspace_size(B, max_q_len, H_kv, D, window,
                                                              max_seq_len)
 
 

@@ -1,72 +1,12 @@
-// C ABI of the 4-bit cache and the step tables: argument checks, workspace
-// layout and launches.  See include/inkling_rel_attn.h for the contracts.
+// C ABI of the 4-bit cache and the step tables, and the calls packed into words.  See include/inkling_rel_attn.h for the contracts.
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
-#include "internal.h"
+#include "api_blocks.h"
 
 using namespace ira;
-
-namespace {
-
-bool cache_shape_ok(int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages) {
-  if (H_kv <= 0 || (D != 64 && D != 128)) return false;
-  return page_size > 0 && page_size % 16 == 0 && page_size <= 256 && num_pages > 0;
-}
-
-// Scratch pages (64 tokens) that hold what a chunk of max_q_len tokens sees.
-int64_t prefill_q4_pages(int32_t max_q_len, int32_t window, int32_t max_seq_len) {
-  int64_t keys = std::max<int32_t>(max_seq_len, 1);
-  // the first visible key is rounded down to a multiple of 64
-  if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + std::max<int32_t>(max_q_len, 0) + 63);
-  return (keys + 63) / 64;
-}
-
-struct PrefillQ4Layout {
-  int64_t pages;  // per sequence
-  size_t table, lens, k, v, total;
-  PrefillQ4Layout(int32_t B, int32_t max_q_len, int32_t H_kv, int32_t D, int32_t window, int32_t max_seq_len) {
-    pages = prefill_q4_pages(max_q_len, window, max_seq_len);
-    const size_t pool = align256((size_t)B * pages * 64 * H_kv * D * 2);
-    table = 0;
-    lens = align256((size_t)B * pages * 4);
-    k = lens + align256((size_t)B * 4);
-    v = k + pool;
-    total = v + pool;
-  }
-};
-
-int rows_q4(bool append, void* k_rows, void* v_rows, const int64_t* slot_map, int32_t T, int32_t H_kv, int32_t D,
-            int32_t page_size, int32_t num_pages, void* k_cache, void* v_cache, int32_t* device_error,
-            void* stream) {
-  if (T < 0 || !cache_shape_ok(H_kv, D, page_size, num_pages)) return INKLING_ERR_ARG;
-  if (H_kv > 65535) return INKLING_ERR_ARG;  // heads are a dimension of the grid
-  if (T == 0) return INKLING_OK;
-  if (!k_rows || !v_rows || !slot_map || !k_cache || !v_cache) return INKLING_ERR_ARG;
-  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(slot_map, 8) || !aligned(device_error, 4))
-    return INKLING_ERR_ALIGN;
-  if (device_info().ok != 1) return INKLING_ERR_DEVICE;
-  Q4RowsCall c;
-  c.k_rows = k_rows;
-  c.v_rows = v_rows;
-  c.k_cache = k_cache;
-  c.v_cache = v_cache;
-  c.slots = slot_map;
-  c.T = T;
-  c.H_kv = H_kv;
-  c.D = D;
-  c.P = page_size;
-  c.num_pages = num_pages;
-  c.dev_err = device_error;
-  c.stream = static_cast<cudaStream_t>(stream);
-  return launch_q4_rows(c, append);
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -122,14 +62,14 @@ int inkling_rel_attn_build_tables_step(const int32_t* seq_lens, const int32_t* n
 int inkling_rel_attn_kv_append_q4(const void* k_new, const void* v_new, const int64_t* slot_map, int32_t T,
                                   int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages, void* k_cache,
                                   void* v_cache, int32_t* device_error, void* stream) {
-  return rows_q4(true, const_cast<void*>(k_new), const_cast<void*>(v_new), slot_map, T, H_kv, D, page_size,
+  return rows_call(launch_q4_rows, true, const_cast<void*>(k_new), const_cast<void*>(v_new), slot_map, T, H_kv, D, page_size,
                  num_pages, k_cache, v_cache, device_error, stream);
 }
 
 int inkling_rel_attn_kv_read_q4(const int64_t* slot_map, const void* k_cache, const void* v_cache, int32_t T,
                                 int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages, void* k_rows,
                                 void* v_rows, int32_t* device_error, void* stream) {
-  return rows_q4(false, k_rows, v_rows, slot_map, T, H_kv, D, page_size, num_pages, const_cast<void*>(k_cache),
+  return rows_call(launch_q4_rows, false, k_rows, v_rows, slot_map, T, H_kv, D, page_size, num_pages, const_cast<void*>(k_cache),
                  const_cast<void*>(v_cache), device_error, stream);
 }
 
@@ -149,52 +89,15 @@ int inkling_rel_attn_decode_q4(const void* q, const void* k_cache, const void* v
                                int32_t num_pages, int32_t R, int32_t window, float scale, void* out,
                                float* lse_out, void* workspace, size_t workspace_bytes, int32_t* device_error,
                                void* stream) {
-  if (B < 0 || q_len < 1 || q_len > 64) return INKLING_ERR_ARG;
-  if (!common_shape_ok(H_q, H_kv, D, page_size, num_pages, R, page_table_stride)) return INKLING_ERR_ARG;
-  if ((int64_t)B * q_len * H_q > INT32_MAX / 4) return INKLING_ERR_ARG;
-  if ((int64_t)num_pages * H_kv > INT32_MAX / (page_size / 16)) return INKLING_ERR_ARG;  // the pool's blocks
-  if (!(scale >= -0x1p54f && scale <= 0x1p54f)) return INKLING_ERR_ARG;  // times 2^73 it stays finite
-  if (B == 0) return INKLING_OK;
-  if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !rel_logits || !out) return INKLING_ERR_ARG;
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
-      !aligned(workspace, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(rel_logits, 4) ||
-      !aligned(lse_out, 4) || !aligned(device_error, 4))
-    return INKLING_ERR_ALIGN;
-  const DevInfo di = device_info();
-  if (di.ok != 1) return INKLING_ERR_DEVICE;
-  const size_t need = decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D, di.sms);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return INKLING_ERR_WORKSPACE;
-  DecodeQ4Call c;
-  c.q = q;
-  c.k_cache = k_cache;
-  c.v_cache = v_cache;
-  c.page_table = page_table;
-  c.pt_stride = page_table_stride;
-  c.seq_lens = seq_lens;
-  c.rel = rel_logits;
-  c.B = B;
-  c.QL = q_len;
-  c.H_q = H_q;
-  c.H_kv = H_kv;
-  c.D = D;
-  c.P = page_size;
-  c.num_pages = num_pages;
-  c.R = R;
-  c.window = window;
-  c.scale = scale;
-  c.out = out;
-  c.lse_out = lse_out;
-  c.workspace = workspace;
-  c.sms = di.sms;
-  c.dev_err = device_error;
-  c.stream = static_cast<cudaStream_t>(stream);
-  return launch_decode_q4(c);
+  return decode_call(launch_decode_q4, q, k_cache, v_cache, page_table, page_table_stride, seq_lens, rel_logits, B, q_len,
+                     H_q, H_kv, D, page_size, num_pages, R, window, scale, out, lse_out, workspace, workspace_bytes,
+                     device_error, stream);
 }
 
 size_t inkling_rel_attn_prefill_q4_workspace_size(int32_t B, int32_t max_q_len, int32_t H_kv, int32_t D,
                                                   int32_t window, int32_t max_seq_len) {
   if (B <= 0 || max_q_len <= 0 || H_kv <= 0 || D <= 0) return 0;
-  return PrefillQ4Layout(B, max_q_len, H_kv, D, window, max_seq_len).total;
+  return ExpandedLayout(B, max_q_len, H_kv, D, window, max_seq_len).total;
 }
 
 int inkling_rel_attn_prefill_q4(const void* q, const int32_t* cu_seqlens_q, const void* k_cache,
@@ -204,73 +107,9 @@ int inkling_rel_attn_prefill_q4(const void* q, const int32_t* cu_seqlens_q, cons
                                 int32_t num_pages, int32_t R, int32_t window, float scale, int32_t max_seq_len,
                                 void* out, float* lse_out, void* workspace, size_t workspace_bytes,
                                 int32_t* device_error, void* stream) {
-  if (B < 0 || T < 0 || max_q_len < 0 || max_seq_len < 0) return INKLING_ERR_ARG;
-  if (!common_shape_ok(H_q, H_kv, D, page_size, num_pages, R, page_table_stride)) return INKLING_ERR_ARG;
-  if (R % 4 != 0) return INKLING_ERR_ARG;
-  if (!(scale == scale)) return INKLING_ERR_ARG;
-  if (B == 0 || T == 0 || max_q_len == 0) return INKLING_OK;
-  if (!q || !cu_seqlens_q || !k_cache || !v_cache || !page_table || !seq_lens || !rel_logits || !out)
-    return INKLING_ERR_ARG;
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
-      !aligned(rel_logits, 16) || !aligned(workspace, 256) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
-      !aligned(cu_seqlens_q, 4) || !aligned(lse_out, 4) || !aligned(device_error, 4))
-    return INKLING_ERR_ALIGN;
-  const PrefillQ4Layout lay(B, max_q_len, H_kv, D, window, max_seq_len);
-  // grid limits of the expansion and of the attention; scratch page ids are int32
-  if (lay.pages * 64 > INT32_MAX - 64 || B * lay.pages > INT32_MAX) return INKLING_ERR_ARG;
-  if ((int64_t)B * ((max_q_len + 127LL) / 128) > 65535) return INKLING_ERR_ARG;
-  if (device_info().ok != 1) return INKLING_ERR_DEVICE;
-  if (!workspace || workspace_bytes < lay.total) return INKLING_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
-  Q4ExpandCall e;
-  e.k_cache = k_cache;
-  e.v_cache = v_cache;
-  e.page_table = page_table;
-  e.pt_stride = page_table_stride;
-  e.cu_seqlens_q = cu_seqlens_q;
-  e.seq_lens = seq_lens;
-  e.B = B;
-  e.H_kv = H_kv;
-  e.D = D;
-  e.P = page_size;
-  e.num_pages = num_pages;
-  e.window = window;
-  e.pages_per_seq = (int32_t)lay.pages;
-  e.k_out = ws + lay.k;
-  e.v_out = ws + lay.v;
-  e.table_out = reinterpret_cast<int32_t*>(ws + lay.table);
-  e.lens_out = reinterpret_cast<int32_t*>(ws + lay.lens);
-  e.dev_err = device_error;
-  e.stream = static_cast<cudaStream_t>(stream);
-  const int rc = launch_q4_expand(e);
-  if (rc != INKLING_OK) return rc;
-  PrefillCall c;
-  c.q = q;
-  c.cu_seqlens_q = cu_seqlens_q;
-  c.k_cache = e.k_out;
-  c.v_cache = e.v_out;
-  c.page_table = e.table_out;
-  c.pt_stride = (int32_t)lay.pages;
-  c.seq_lens = e.lens_out;
-  c.rel = rel_logits;
-  c.B = B;
-  c.T = T;
-  c.max_q_len = max_q_len;
-  c.H_q = H_q;
-  c.H_kv = H_kv;
-  c.D = D;
-  c.P = 64;
-  c.num_pages = (int32_t)(B * lay.pages);
-  c.R = R;
-  c.window = window;
-  c.scale = scale;
-  c.max_seq_len = (int32_t)(lay.pages * 64);
-  c.out = out;
-  c.lse_out = lse_out;
-  c.dev_err = device_error;
-  c.stream = static_cast<cudaStream_t>(stream);
-  c.after_expansion = true;
-  return launch_prefill(c);
+  return prefill_call(launch_q4_expand, q, cu_seqlens_q, k_cache, v_cache, page_table, page_table_stride, seq_lens,
+                      rel_logits, B, T, max_q_len, H_q, H_kv, D, page_size, num_pages, R, window, scale, max_seq_len, out,
+                      lse_out, workspace, workspace_bytes, device_error, stream);
 }
 
 int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
@@ -311,7 +150,9 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
                                                 num_pages, max_tokens, kv_lens, cu, slots, left, step, err, stream);
     }
     case INKLING_PACKED_KV_APPEND_Q4:
-    case INKLING_PACKED_KV_READ_Q4: {
+    case INKLING_PACKED_KV_READ_Q4:
+    case INKLING_PACKED_KV_APPEND_Q8:
+    case INKLING_PACKED_KV_READ_Q8: {
       if (count != 12) return INKLING_ERR_ARG;
       void *x = ptr(), *y = ptr(), *z = ptr();
       const int32_t T = i32(), H_kv = i32(), D = i32(), page_size = i32(), num_pages = i32();
@@ -319,13 +160,16 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
       int32_t* err = static_cast<int32_t*>(ptr());
       void* stream = ptr();
       if (!fits) return INKLING_ERR_ARG;
-      if (call == INKLING_PACKED_KV_APPEND_Q4)
-        return inkling_rel_attn_kv_append_q4(x, y, static_cast<const int64_t*>(z), T, H_kv, D, page_size, num_pages, u,
-                                             w, err, stream);
-      return inkling_rel_attn_kv_read_q4(static_cast<const int64_t*>(x), y, z, T, H_kv, D, page_size, num_pages, u, w,
-                                         err, stream);
+      if (call == INKLING_PACKED_KV_APPEND_Q4 || call == INKLING_PACKED_KV_APPEND_Q8) {
+        const auto append =
+            call == INKLING_PACKED_KV_APPEND_Q4 ? inkling_rel_attn_kv_append_q4 : inkling_rel_attn_kv_append_q8;
+        return append(x, y, static_cast<const int64_t*>(z), T, H_kv, D, page_size, num_pages, u, w, err, stream);
+      }
+      const auto read = call == INKLING_PACKED_KV_READ_Q4 ? inkling_rel_attn_kv_read_q4 : inkling_rel_attn_kv_read_q8;
+      return read(static_cast<const int64_t*>(x), y, z, T, H_kv, D, page_size, num_pages, u, w, err, stream);
     }
-    case INKLING_PACKED_DECODE_Q4: {
+    case INKLING_PACKED_DECODE_Q4:
+    case INKLING_PACKED_DECODE_Q8: {
       if (count != 23) return INKLING_ERR_ARG;
       const void *q = ptr(), *k = ptr(), *v = ptr();
       const int32_t* table = ci();
@@ -341,10 +185,12 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
       const size_t ws_bytes = (size_t)a[at++];
       int32_t* err = static_cast<int32_t*>(ptr());
       if (!fits) return INKLING_ERR_ARG;
-      return inkling_rel_attn_decode_q4(q, k, v, table, stride, seq_lens, rel, B, q_len, H_q, H_kv, D, page_size,
-                                        num_pages, R, window, scale, out, lse, ws, ws_bytes, err, ptr());
+      const auto decode = call == INKLING_PACKED_DECODE_Q4 ? inkling_rel_attn_decode_q4 : inkling_rel_attn_decode_q8;
+      return decode(q, k, v, table, stride, seq_lens, rel, B, q_len, H_q, H_kv, D, page_size, num_pages, R, window,
+                    scale, out, lse, ws, ws_bytes, err, ptr());
     }
-    case INKLING_PACKED_PREFILL_Q4: {
+    case INKLING_PACKED_PREFILL_Q4:
+    case INKLING_PACKED_PREFILL_Q8: {
       if (count != 26) return INKLING_ERR_ARG;
       const void* q = ptr();
       const int32_t* cu = ci();
@@ -363,9 +209,10 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
       const size_t ws_bytes = (size_t)a[at++];
       int32_t* err = static_cast<int32_t*>(ptr());
       if (!fits) return INKLING_ERR_ARG;
-      return inkling_rel_attn_prefill_q4(q, cu, k, v, table, stride, seq_lens, rel, B, T, max_q_len, H_q, H_kv, D,
-                                         page_size, num_pages, R, window, scale, max_seq_len, out, lse, ws, ws_bytes,
-                                         err, ptr());
+      const auto prefill =
+          call == INKLING_PACKED_PREFILL_Q4 ? inkling_rel_attn_prefill_q4 : inkling_rel_attn_prefill_q8;
+      return prefill(q, cu, k, v, table, stride, seq_lens, rel, B, T, max_q_len, H_q, H_kv, D, page_size, num_pages, R,
+                     window, scale, max_seq_len, out, lse, ws, ws_bytes, err, ptr());
     }
   }
   return INKLING_ERR_ARG;

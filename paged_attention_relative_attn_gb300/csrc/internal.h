@@ -112,8 +112,8 @@ struct KvConvCall {
   cudaStream_t stream;
 };
 
-// Rows of the 4-bit cache by slot: appended (k_rows, v_rows read) or read back (written).
-struct Q4RowsCall {
+// Rows of the 4-bit or 8-bit cache by slot: appended (k_rows, v_rows read) or read back (written).
+struct RowsCall {
   void* k_rows;
   void* v_rows;
   void* k_cache;
@@ -125,7 +125,7 @@ struct Q4RowsCall {
 };
 
 // The visible part of a batch's sequences, expanded into bf16 pages of 64 tokens.
-struct Q4ExpandCall {
+struct ExpandCall {
   const void* k_cache;
   const void* v_cache;
   const int32_t* page_table;
@@ -141,7 +141,7 @@ struct Q4ExpandCall {
   cudaStream_t stream;
 };
 
-struct DecodeQ4Call {
+struct DecodeBlocksCall {
   const void* q;
   const void* k_cache;
   const void* v_cache;
@@ -179,10 +179,14 @@ struct TablesCall {
 };
 
 int launch_decode(const DecodeCall& c);        // returns INKLING_* code
-int launch_q4_rows(const Q4RowsCall& c, bool append);
-int launch_q4_expand(const Q4ExpandCall& c);
-int launch_decode_q4(const DecodeQ4Call& c);
+int launch_q4_rows(const RowsCall& c, bool append);
+int launch_q8_rows(const RowsCall& c, bool append);
+int launch_q4_expand(const ExpandCall& c);
+int launch_q8_expand(const ExpandCall& c);
+int launch_decode_q4(const DecodeBlocksCall& c);
+int launch_decode_q8(const DecodeBlocksCall& c);
 int launch_build_tables(const TablesCall& c);
+// of decode over the 4-bit or 8-bit cache
 size_t decode_q4_workspace_bytes(int32_t B, int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms);
 int launch_prefill(const PrefillCall& c);      // returns INKLING_* code
 int launch_kv_append(const KvAppendCall& c);   // returns INKLING_* code

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include "async.cuh"
+#include "expand.cuh"
 #include "internal.h"
 #include "launch.h"
 #include "plan.cuh"
@@ -24,7 +25,6 @@
 
 namespace ira {
 
-constexpr int kRowThreads = 256;
 constexpr int kQ4Heads = 2;           // heads per thread of a large call (8192 tokens x 16 heads both ways: 30 us; 1: 33.7, 4: 31.9)
 constexpr int kRowsFill = 4;          // such blocks per SM from which on it is taken
 
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-static Q4RowsParams rows_params(const Q4RowsCall& c) {
+static Q4RowsParams rows_params(const RowsCall& c) {
   Q4RowsParams p;
   p.k_rows = static_cast<uint4*>(c.k_rows);
   p.v_rows = static_cast<uint4*>(c.v_rows);
@@ -176,7 +176,7 @@ static bool rows_launch(const Q4RowsParams& p, bool append, cudaStream_t stream)
                 : launch_dependent(kv_read_q4_kernel<D, HEADS>, g, kRowThreads, 0, p, stream);
 }
 
-int launch_q4_rows(const Q4RowsCall& c, bool append) {
+int launch_q4_rows(const RowsCall& c, bool append) {
   const Q4RowsParams p = rows_params(c);
   // Several heads per thread share its place in the cache; a call that could not fill
   // the GPU so is latency-bound and takes a head per thread.  Append and read, blocks at
@@ -191,100 +191,27 @@ int launch_q4_rows(const Q4RowsCall& c, bool append) {
 }
 
 // ---------------------------------------------------------------------------
-// Expansion for prefill: the keys that any query of sequence b's chunk sees,
-// [lo_b, L_b), go to bf16 pages of 64 tokens of the scratch pool, sequence b's
-// from page b * pages_per_seq on.  Its first key is base_b = lo_b rounded down
-// to 64, so the scratch sequence has length L_b - base_b; relative positions,
-// all that the attention uses, stay the same.  The scratch lengths and page
-// table are written for the attention that follows.  A sequence that the
-// scratch cannot hold, or whose chunk is longer than it is, gets length 0,
-// which the attention reports and skips.
-struct Q4ExpandParams {
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
-  const int32_t* page_table;
-  const int32_t* cu;
-  const int32_t* seq_lens;
-  uint4* k_out;  // [B * pages_per_seq][64][H_kv][D / 8]
-  uint4* v_out;
-  int32_t* table_out;  // [B][pages_per_seq]
-  int32_t* lens_out;   // [B]
-  int32_t* dev_err;
-  int B, H_kv, P, num_pages, pt_stride, window, pages_per_seq;
+// Expansion for prefill (expand.cuh)
+struct Q4ReadFormat {
+  __host__ __device__ static constexpr int block_bytes(int D) { return q4_block_bytes(D); }
+  template <int D>
+  __device__ static __forceinline__ void read8(const uint8_t* kb, const uint8_t* vb, bool have, int r, int i, uint4& k,
+                                               uint4& v) {
+    q4_read8<D>(kb, vb, have, r, i >> 2, i & 3, k, v);
+  }
 };
-
-constexpr int kExpandTokens = 16;  // tokens per block of the grid
-constexpr int kExpandBlocks = 2;   // blocks that share the heads of these tokens (local chunk 302.0 -> 299.3 us)
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
-    q4_expand_kernel(const __grid_constant__ Q4ExpandParams p) {
+    q4_expand_kernel(const __grid_constant__ ExpandParams p) {
   await_previous_kernel();
-  constexpr int U = D / 8;
-  const int b = blockIdx.y;
-  const int q_len = p.cu[b + 1] - p.cu[b];
-  const int L_in = p.seq_lens[b];
-  const int L = min(max(L_in, 0), p.pt_stride * p.P);
-  const int lo = p.window > 0 ? max(0, L - q_len - p.window + 1) : 0;
-  const int base = lo & ~63;
-  const bool fits = q_len > 0 && q_len <= L && L - base <= p.pages_per_seq * 64;
-  if (blockIdx.x == 0 && blockIdx.z == 0) {
-    if (threadIdx.x == 0) {
-      p.lens_out[b] = fits ? L - base : 0;
-      if (L_in > L || (q_len > 0 && q_len <= L && !fits)) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
-    }
-    for (int i = threadIdx.x; i < p.pages_per_seq; i += kRowThreads)
-      p.table_out[(size_t)b * p.pages_per_seq + i] = b * p.pages_per_seq + i;
-  }
-  const int j0 = base + (int)blockIdx.x * kExpandTokens;  // all in one 16-token block of the cache
-  if (!fits || j0 >= L || j0 + kExpandTokens <= lo) return;  // keys before lo are not attended to: their page may be gone
-  const int lp = j0 / p.P;
-  const int page = p.page_table[(size_t)b * p.pt_stride + lp];
-  const bool ok = page >= 0 && page < p.num_pages;
-  if (!ok && threadIdx.x == 0) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
-  // thread: 8 channels of one row, head after head (with D = 64 half of the block has every other head)
-  constexpr int kHeads = kRowThreads / (kExpandTokens * U);
-  const int i = threadIdx.x % U, r = threadIdx.x / U % kExpandTokens;
-  const bool in = r < L - j0;
-  const size_t block = q4_block_at(0, 1, 0, 1, p.P, D);  // from one head's first block to the next's
-  const size_t at = q4_block_at(ok ? page : 0, 0, j0 - lp * p.P, p.H_kv, p.P, D);
-  const size_t dst = ((size_t)b * p.pages_per_seq * 64 + (j0 - base) + r) * p.H_kv * U + i;
-#pragma unroll 4
-  for (int h0 = kHeads * blockIdx.z; h0 < p.H_kv; h0 += kHeads * gridDim.z) {
-    const int h = h0 + threadIdx.x / (kExpandTokens * U);
-    const bool mine = in && h < p.H_kv;
-    const size_t src = at + (size_t)h * block;
-    uint4 k, v;
-    q4_read8<D>(p.k_cache + src, p.v_cache + src, ok && mine, r, i >> 2, i & 3, k, v);
-    if (mine) {
-      p.k_out[dst + (size_t)h * U] = k;
-      p.v_out[dst + (size_t)h * U] = v;
-    }
-  }
+  expand_blocks<Q4ReadFormat, D>(p);
 }
 
-int launch_q4_expand(const Q4ExpandCall& c) {
-  Q4ExpandParams p;
-  p.k_cache = static_cast<const uint8_t*>(c.k_cache);
-  p.v_cache = static_cast<const uint8_t*>(c.v_cache);
-  p.page_table = c.page_table;
-  p.cu = c.cu_seqlens_q;
-  p.seq_lens = c.seq_lens;
-  p.k_out = static_cast<uint4*>(c.k_out);
-  p.v_out = static_cast<uint4*>(c.v_out);
-  p.table_out = c.table_out;
-  p.lens_out = c.lens_out;
-  p.dev_err = c.dev_err;
-  p.B = c.B;
-  p.H_kv = c.H_kv;
-  p.P = c.P;
-  p.num_pages = c.num_pages;
-  p.pt_stride = c.pt_stride;
-  p.window = c.window;
-  p.pages_per_seq = c.pages_per_seq;
-  const dim3 grid((unsigned)(c.pages_per_seq * (64 / kExpandTokens)), (unsigned)c.B, kExpandBlocks);
-  const bool ok = c.D == 128 ? launch_dependent(q4_expand_kernel<128>, grid, kRowThreads, 0, p, c.stream)
-                             : launch_dependent(q4_expand_kernel<64>, grid, kRowThreads, 0, p, c.stream);
+int launch_q4_expand(const ExpandCall& c) {
+  const ExpandParams p = expand_params(c);
+  const bool ok = c.D == 128 ? launch_dependent(q4_expand_kernel<128>, expand_grid(c), kRowThreads, 0, p, c.stream)
+                             : launch_dependent(q4_expand_kernel<64>, expand_grid(c), kRowThreads, 0, p, c.stream);
   return ok ? INKLING_OK : INKLING_ERR_CUDA;
 }
 

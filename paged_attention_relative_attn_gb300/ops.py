@@ -249,7 +249,7 @@ def kv_conv_append(k_new, v_new, cu_seqlens_q, seq_lens, page_table, k_cache, v_
 
 
 # ---------------------------------------------------------------------------
-# Step tables and the 4-bit cache
+# Step tables, and the caches held in 4 and in 8 bits
 # ---------------------------------------------------------------------------
 
 # A decode step calls several of these with a few microseconds of GPU work each, so their
@@ -314,18 +314,24 @@ def _workspace(workspace, need, q):
     return workspace, workspace.nbytes
 
 
-def _q4_cache(k_cache, v_cache):
-    """(num_pages, H_kv, page_size, D) of a pair of 4-bit pools; their devices are the caller's check."""
+# The 4-bit and the 8-bit cache differ in their calls and in the bytes of a token's row of one KV head.
+_CACHES = {"q4": ("9 * D / 16", {36: 64, 72: 128}), "q8": ("D + 1", {65: 64, 129: 128})}
+
+
+def _block_cache(kind, k_cache, v_cache):
+    """(num_pages, H_kv, page_size, D) of a pair of 4-bit or 8-bit pools; their devices are the caller's check."""
+    last, rows = _CACHES[kind]
     if k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or k_cache.dim() != 4:
-        raise TypeError("k_cache, v_cache: uint8 pools [num_pages, H_kv, page_size, 9 * D / 16] expected")
+        raise TypeError(f"k_cache, v_cache: uint8 pools [num_pages, H_kv, page_size, {last}] expected")
     n, H_kv, P, row = k_cache.shape
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if row not in (36, 72):
-        raise ValueError(f"k_cache: rows of {row} bytes; 36 (D = 64) or 72 (D = 128) expected")
+    if row not in rows:
+        raise ValueError(f"k_cache: rows of {row} bytes; "
+                         + " or ".join(f"{b} (D = {D})" for b, D in rows.items()) + " expected")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k_cache, v_cache: must be contiguous")
-    return n, H_kv, P, row * 16 // 9
+    return n, H_kv, P, rows[row]
 
 
 def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page_size, max_tokens=None,
@@ -395,17 +401,10 @@ def build_tables(seq_lens, new_lens, page_table, free_pages, free_count, *, page
     return kv_lens, cu_seqlens_q, slot_map, free_left
 
 
-def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None, stream=None):
-    """Quantise the new tokens' K/V rows into the 4-bit paged cache (in place).
-    See inkling_rel_attn_kv_append_q4.
-
-    k_new, v_new [T, H_kv, D] bf16; slot_map [T] int64 (page * page_size + place,
-    negative: skipped); k_cache, v_cache [num_pages, H_kv, page_size, 9 * D / 16]
-    uint8.
-    """
+def _append_rows(kind, k_new, v_new, slot_map, k_cache, v_cache, device_error, stream):
     if stream is not None:
         _own_stream(stream, k_new)
-    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    n, H_kv, P, D = _block_cache(kind, k_cache, v_cache)
     T = slot_map.numel()
     dev = k_new.get_device()
     if not (k_new.dtype is v_new.dtype is _BF16 and slot_map.dtype is _I64
@@ -414,20 +413,40 @@ def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None,
             and k_new.shape == v_new.shape == (T, H_kv, D) and slot_map.dim() == 1):
         _refuse(dev, ((k_new, "k_new", _BF16, 3), (v_new, "v_new", _BF16, 3), (slot_map, "slot_map", _I64, 1),
                       (k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4)))
-    _launch("inkling_rel_attn_kv_append_q4", dev, stream,
+    _launch(f"inkling_rel_attn_kv_append_{kind}", dev, stream,
             k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), T, H_kv, D, P, n,
             k_cache.data_ptr(), v_cache.data_ptr(), _error_word(device_error, dev))
 
 
-def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_error=None, stream=None):
-    """Rows of the 4-bit cache as the bf16 values they stand for.  See
-    inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
+def kv_append_q4(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None, stream=None):
+    """Quantise the new tokens' K/V rows into the 4-bit paged cache (in place).
+    See inkling_rel_attn_kv_append_q4.
+
+    k_new, v_new [T, H_kv, D] bf16; slot_map [T] int64 (page * page_size + place,
+    negative: skipped); k_cache, v_cache [num_pages, H_kv, page_size, 9 * D / 16]
+    uint8.
     """
+    _append_rows("q4", k_new, v_new, slot_map, k_cache, v_cache, device_error, stream)
+
+
+def kv_append_q8(k_new, v_new, slot_map, k_cache, v_cache, *, device_error=None, stream=None):
+    """Quantise the new tokens' K/V rows into the 8-bit paged cache (in place).
+    See inkling_rel_attn_kv_append_q8.
+
+    k_new, v_new [T, H_kv, D] bf16; slot_map [T] int64 (page * page_size + place,
+    negative: skipped; the tokens of one block of 16 places within 16 of the call,
+    as build_tables gives them); k_cache, v_cache [num_pages, H_kv, page_size, D + 1]
+    uint8, zeros before their first use.
+    """
+    _append_rows("q8", k_new, v_new, slot_map, k_cache, v_cache, device_error, stream)
+
+
+def _read_rows(kind, slot_map, k_cache, v_cache, k_rows, v_rows, device_error, stream):
     if stream is not None:  # buffers made here are that stream's
         _own_stream(stream, k_cache)
         with torch.cuda.stream(stream):
-            return kv_read_q4(slot_map, k_cache, v_cache, k_rows=k_rows, v_rows=v_rows, device_error=device_error)
-    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+            return _read_rows(kind, slot_map, k_cache, v_cache, k_rows, v_rows, device_error, None)
+    n, H_kv, P, D = _block_cache(kind, k_cache, v_cache)
     T = slot_map.numel()
     if k_rows is None:
         k_rows = torch.empty((T, H_kv, D), dtype=_BF16, device=k_cache.device)
@@ -440,32 +459,41 @@ def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_e
             and k_rows.shape == v_rows.shape == (T, H_kv, D) and slot_map.dim() == 1):
         _refuse(dev, ((k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4), (slot_map, "slot_map", _I64, 1),
                       (k_rows, "k_rows", _BF16, 3), (v_rows, "v_rows", _BF16, 3)))
-    _launch("inkling_rel_attn_kv_read_q4", dev, None,
+    _launch(f"inkling_rel_attn_kv_read_{kind}", dev, None,
             slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H_kv, D, P, n,
             k_rows.data_ptr(), v_rows.data_ptr(), _error_word(device_error, dev))
     return k_rows, v_rows
+
+
+def kv_read_q4(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_error=None, stream=None):
+    """Rows of the 4-bit cache as the bf16 values they stand for.  See
+    inkling_rel_attn_kv_read_q4.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
+    """
+    return _read_rows("q4", slot_map, k_cache, v_cache, k_rows, v_rows, device_error, stream)
+
+
+def kv_read_q8(slot_map, k_cache, v_cache, *, k_rows=None, v_rows=None, device_error=None, stream=None):
+    """Rows of the 8-bit cache as the bf16 values they stand for.  See
+    inkling_rel_attn_kv_read_q8.  Returns (k_rows, v_rows) [T, H_kv, D] bf16.
+    """
+    return _read_rows("q8", slot_map, k_cache, v_cache, k_rows, v_rows, device_error, stream)
 
 
 def decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D, num_sms=0):
     return _lib.inkling_rel_attn_decode_q4_workspace_size(B, q_len, H_q, H_kv, D, num_sms)
 
 
-def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1, window, scale, out=None,
-              lse=None, workspace=None, device_error=None, stream=None):
-    """Decode of the last ``q_len`` tokens of each sequence over the 4-bit cache.
-    See inkling_rel_attn_decode_q4.
+def decode_q8_workspace_bytes(B, q_len, H_q, H_kv, D, num_sms=0):
+    return _lib.inkling_rel_attn_decode_q8_workspace_size(B, q_len, H_q, H_kv, D, num_sms)
 
-    q [B * q_len, H_q, D] bf16 (row b * q_len + i); k_cache, v_cache [num_pages,
-    H_kv, page_size, 9 * D / 16] uint8; page_table [B, stride] int32; seq_lens
-    [B] int32; rel_logits [B * q_len, H_q, R] fp32.  Returns (out bf16 like q,
-    lse fp32 [B * q_len, H_q]).  Pass ``out``, ``lse`` and ``workspace``
-    (decode_q4_workspace_bytes) to avoid allocations.
-    """
+
+def _decode_blocks(kind, q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len, window, scale, out, lse, workspace,
+                   device_error, stream):
     if stream is not None:  # buffers made here are that stream's
         _own_stream(stream, q)
         with torch.cuda.stream(stream):
-            return decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len=q_len, window=window,
-                             scale=scale, out=out, lse=lse, workspace=workspace, device_error=device_error)
+            return _decode_blocks(kind, q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len, window, scale, out,
+                                  lse, workspace, device_error, None)
     try:
         (T, H_q, _), (rel_T, rel_H, R), (rows, stride), (B,) = (q.shape, rel_logits.shape, page_table.shape,
                                                                 seq_lens.shape)
@@ -475,7 +503,7 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
-    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    n, H_kv, P, D = _block_cache(kind, k_cache, v_cache)
     dev = q.get_device()
     if not (q.dtype is out.dtype is _BF16 and page_table.dtype is seq_lens.dtype is _I32
             and rel_logits.dtype is lse.dtype is _F32
@@ -489,7 +517,7 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
                       (page_table, "page_table", _I32, 2), (seq_lens, "seq_lens", _I32, 1),
                       (rel_logits, "rel_logits", _F32, 3), (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
     workspace, ws_bytes = _workspace(workspace, lambda: decode_q4_workspace_bytes(B, q_len, H_q, H_kv, D), q)
-    _launch("inkling_rel_attn_decode_q4", dev, None,
+    _launch(f"inkling_rel_attn_decode_{kind}", dev, None,
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), stride,
             seq_lens.data_ptr(), rel_logits.data_ptr(), B, q_len, H_q, H_kv, D, P, n, R,
             window, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes,
@@ -497,26 +525,50 @@ def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1,
     return out, lse
 
 
+def decode_q4(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1, window, scale, out=None,
+              lse=None, workspace=None, device_error=None, stream=None):
+    """Decode of the last ``q_len`` tokens of each sequence over the 4-bit cache.
+    See inkling_rel_attn_decode_q4.
+
+    q [B * q_len, H_q, D] bf16 (row b * q_len + i); k_cache, v_cache [num_pages,
+    H_kv, page_size, 9 * D / 16] uint8; page_table [B, stride] int32; seq_lens
+    [B] int32; rel_logits [B * q_len, H_q, R] fp32.  Returns (out bf16 like q,
+    lse fp32 [B * q_len, H_q]).  Pass ``out``, ``lse`` and ``workspace``
+    (decode_q4_workspace_bytes) to avoid allocations.
+    """
+    return _decode_blocks("q4", q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len, window, scale, out, lse,
+                          workspace, device_error, stream)
+
+
+def decode_q8(q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, q_len=1, window, scale, out=None,
+              lse=None, workspace=None, device_error=None, stream=None):
+    """Decode of the last ``q_len`` tokens of each sequence over the 8-bit cache.
+    See inkling_rel_attn_decode_q8.
+
+    k_cache, v_cache [num_pages, H_kv, page_size, D + 1] uint8; the rest as for
+    ``decode_q4``.  Returns (out bf16 like q, lse fp32 [B * q_len, H_q]).  Pass
+    ``out``, ``lse`` and ``workspace`` (decode_q8_workspace_bytes) to avoid
+    allocations.
+    """
+    return _decode_blocks("q8", q, k_cache, v_cache, page_table, seq_lens, rel_logits, q_len, window, scale, out, lse,
+                          workspace, device_error, stream)
+
+
 def prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len):
     return _lib.inkling_rel_attn_prefill_q4_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len)
 
 
-def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, window, scale,
-               max_seq_len, max_q_len, out=None, lse=None, workspace=None, device_error=None, stream=None):
-    """Chunked / paged prefill over the 4-bit cache.  See inkling_rel_attn_prefill_q4.
+def prefill_q8_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len):
+    return _lib.inkling_rel_attn_prefill_q8_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len)
 
-    q [T, H_q, D] bf16; cu_seqlens_q [B + 1] int32; rel_logits [T, H_q, R] fp32;
-    the cache, page_table and seq_lens as for ``decode_q4``; max_seq_len and
-    max_q_len are host bounds.  Returns (out bf16 [T, H_q, D], lse fp32 [T, H_q]).
-    Pass ``out``, ``lse`` and ``workspace`` (prefill_q4_workspace_bytes) to avoid
-    allocations.
-    """
+
+def _prefill_blocks(kind, q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window, scale, max_seq_len,
+                    max_q_len, out, lse, workspace, device_error, stream):
     if stream is not None:  # buffers made here are that stream's
         _own_stream(stream, q)
         with torch.cuda.stream(stream):
-            return prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window=window,
-                              scale=scale, max_seq_len=max_seq_len, max_q_len=max_q_len, out=out, lse=lse,
-                              workspace=workspace, device_error=device_error)
+            return _prefill_blocks(kind, q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window,
+                                   scale, max_seq_len, max_q_len, out, lse, workspace, device_error, None)
     try:
         (T, H_q, _), (rel_T, rel_H, R), (rows, stride), (B,) = (q.shape, rel_logits.shape, page_table.shape,
                                                                 seq_lens.shape)
@@ -526,7 +578,7 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
-    n, H_kv, P, D = _q4_cache(k_cache, v_cache)
+    n, H_kv, P, D = _block_cache(kind, k_cache, v_cache)
     dev = q.get_device()
     if not (q.dtype is out.dtype is _BF16
             and page_table.dtype is seq_lens.dtype is cu_seqlens_q.dtype is _I32
@@ -543,12 +595,38 @@ def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
                       (out, "out", _BF16, 3), (lse, "lse", _F32, 2)))
     workspace, ws_bytes = _workspace(
         workspace, lambda: prefill_q4_workspace_bytes(B, max_q_len, H_kv, D, window, max_seq_len), q)
-    _launch("inkling_rel_attn_prefill_q4", dev, None,
+    _launch(f"inkling_rel_attn_prefill_{kind}", dev, None,
             q.data_ptr(), cu_seqlens_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             page_table.data_ptr(), stride, seq_lens.data_ptr(), rel_logits.data_ptr(), B, T,
             max_q_len, H_q, H_kv, D, P, n, R, window, scale, max_seq_len, out.data_ptr(),
             lse.data_ptr(), workspace.data_ptr(), ws_bytes, _error_word(device_error, dev))
     return out, lse
+
+
+def prefill_q4(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, window, scale,
+               max_seq_len, max_q_len, out=None, lse=None, workspace=None, device_error=None, stream=None):
+    """Chunked / paged prefill over the 4-bit cache.  See inkling_rel_attn_prefill_q4.
+
+    q [T, H_q, D] bf16; cu_seqlens_q [B + 1] int32; rel_logits [T, H_q, R] fp32;
+    the cache, page_table and seq_lens as for ``decode_q4``; max_seq_len and
+    max_q_len are host bounds.  Returns (out bf16 [T, H_q, D], lse fp32 [T, H_q]).
+    Pass ``out``, ``lse`` and ``workspace`` (prefill_q4_workspace_bytes) to avoid
+    allocations.
+    """
+    return _prefill_blocks("q4", q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window, scale,
+                           max_seq_len, max_q_len, out, lse, workspace, device_error, stream)
+
+
+def prefill_q8(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, *, window, scale,
+               max_seq_len, max_q_len, out=None, lse=None, workspace=None, device_error=None, stream=None):
+    """Chunked / paged prefill over the 8-bit cache.  See inkling_rel_attn_prefill_q8.
+
+    k_cache, v_cache [num_pages, H_kv, page_size, D + 1] uint8; the rest as for
+    ``prefill_q4``.  Returns (out bf16 [T, H_q, D], lse fp32 [T, H_q]).  Pass ``out``,
+    ``lse`` and ``workspace`` (prefill_q8_workspace_bytes) to avoid allocations.
+    """
+    return _prefill_blocks("q8", q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logits, window, scale,
+                           max_seq_len, max_q_len, out, lse, workspace, device_error, stream)
 
 
 def decode_inputs(inp, **kw):
