@@ -321,46 +321,21 @@ struct Q4Format {
   };
 };
 
-template <int D, bool MULTI>
-__global__ void __launch_bounds__(kRunThreads, kRunCtas)
-    decode_q4_kernel(const __grid_constant__ DecodeBlocksParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  decode_blocks_set_up<Q4Format, D>(p, smem);
-  await_previous_kernel();
-  decode_blocks<Q4Format, D, MULTI>(p, smem);
-}
-
-template <int D>
-__global__ void __launch_bounds__(32 * kRunMergeWarps) merge_q4_kernel(const __grid_constant__ DecodeBlocksParams p) {
-  await_previous_kernel();
-  merge_parts<D>(p);
-}
-
 size_t decode_q4_workspace_bytes(int32_t, int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms) {
   return RunPlan(QL, H_q, H_kv, D, sms).total;
 }
 
-template <int D, bool MULTI>
-static int launch_decode_q4_t(const DecodeBlocksCall& c, DecodeBlocksParams prm, const RunPlan& plan) {
-  prm.slots = run_slots(q4_block_bytes(D), D, plan.NR);
-  const int smem = RunSmem(q4_block_bytes(D), D, plan.NR, prm.slots).total;
-  auto kern = decode_q4_kernel<D, MULTI>;
-  static std::atomic<int> limit_set[kMaxDevices];
-  if (!smem_limit_on_device(reinterpret_cast<const void*>(kern), kRunSmemBudget, limit_set)) return INKLING_ERR_CUDA;
-  if (!launch_dependent(kern, dim3(plan.grid), kRunThreads, smem, prm, c.stream)) return INKLING_ERR_CUDA;
-  if (!launch_dependent(merge_q4_kernel<D>, dim3(plan.grid, plan.NR), 32 * kRunMergeWarps, 0, prm, c.stream))
-    return INKLING_ERR_CUDA;
-  return INKLING_OK;
-}
+struct Q4Launch {
+  template <int D, bool MULTI>
+  static bool launch(const DecodeBlocksCall& c, const DecodeBlocksParams& p, const RunPlan& plan, int smem) {
+    auto kern = decode_blocks_kernel<Q4Format, D, MULTI>;
+    static std::atomic<int> limit_set[kMaxDevices];
+    return smem_limit_on_device(reinterpret_cast<const void*>(kern), kRunSmemBudget, limit_set) &&
+           launch_dependent(kern, dim3(plan.grid), kRunThreads, smem, p, c.stream) &&
+           launch_dependent(merge_blocks_kernel<D>, dim3(plan.grid, plan.NR), 32 * kRunMergeWarps, 0, p, c.stream);
+  }
+};
 
-int launch_decode_q4(const DecodeBlocksCall& c) {
-  const RunPlan plan(c.QL, c.H_q, c.H_kv, c.D, c.sms);
-  if (!run_countable(c, plan)) return INKLING_ERR_ARG;
-  DecodeBlocksParams p = run_params(c, plan);
-  p.scale = c.scale * kDown;
-  if (c.D == 128)
-    return plan.TG == 1 ? launch_decode_q4_t<128, false>(c, p, plan) : launch_decode_q4_t<128, true>(c, p, plan);
-  return plan.TG == 1 ? launch_decode_q4_t<64, false>(c, p, plan) : launch_decode_q4_t<64, true>(c, p, plan);
-}
+int launch_decode_q4(const DecodeBlocksCall& c) { return launch_blocks<Q4Format, Q4Launch>(c, c.scale * kDown); }
 
 }  // namespace ira
