@@ -34,6 +34,7 @@
 //   key_of(g)        key of a block that row g < 8 of its first operand stands for; row g + 8: 8 more
 //   zero_block       a block that reads as zeros, at two places of shared memory (K, V)
 //   prepare          q of an item's rows as operands, and up to 4 words beside (RunPrep::extra)
+//   kGroup           tiles whose copies go out together (those of a long ring)
 //   Consumer         the products S^T = K Q^T (16 keys x rows) and O^T += V^T P^T of a warp
 #pragma once
 
@@ -295,37 +296,44 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
       for (int i = 0; i < 3; ++i) dst[32 * i] = src[i];
     };
     // ---- the sum of the warps' parts of an item
-    // lane W * r + w makes the factor of warp w's part of row r.  (Short code: this warp
-    // shares the instruction cache with the consumers' loop; unrolled by 4, 11 us more
-    // for 64 sequences of 4 drafts.)
+    // lane W * r + w makes the factor of warp w's part of row r, and leaves it where the part's
+    // maximum was.  No shuffles: beside waiting and computing warps one takes some 280 cycles
+    // here, and the four a row were what held the items up (64 sequences of 4 drafts over the
+    // 8-bit cache).  (Short code: this warp shares the instruction cache with
+    // the consumers' loop; unrolled by 4, 11 us more for 64 sequences of 4 drafts.)
     auto join = [&](const RunItem& it, int cb) {
       static_assert(W * HP == 32, "a lane per row and warp");
       constexpr int LR = D / 4;  // lanes per row
       const float* co = comb_o(cb);
-      const float* cm = comb_m(cb);
-      const int rows = it.tn * it.heads, d = 4 * (lane % LR);
-      const float m = cm[lane % W * HP + lane / W];
-      float M = m;
+      float* cm = comb_m(cb);
+      const int rows = it.tn * it.heads, d = 4 * (lane % LR), row = lane / W;
+      float m[W], M = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int off = 1; off < W; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      float f = ex2((m - (M == -INFINITY ? 0.f : M)) * kLog2e);
-      float l = f * cm[(W + lane % W) * HP + lane / W];
+      for (int w = 0; w < W; ++w) {
+        m[w] = cm[w * HP + row];
+        M = fmaxf(M, m[w]);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
-      for (int off = 1; off < W; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-      const bool mine = lane % W == 0 && lane / W < rows;
+      for (int w = 0; w < W; ++w) l = fmaf(ex2((m[w] - base) * kLog2e), cm[(W + w) * HP + row], l);
+      __syncwarp();
+      float f = ex2((cm[lane % W * HP + row] - base) * kLog2e);
+      const bool mine = lane % W == 0 && row < rows;
       if (it.part < 0) {
         f *= l == 0.f ? 0.f : __fdividef(1.f, l);  // every score -inf: an empty row
-        if (mine && p.lse_out) p.lse_out[row_of(it, lane / W)] = M + logf(l);
+        if (mine && p.lse_out) p.lse_out[row_of(it, row)] = M + logf(l);
       } else if (mine) {
-        p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + lane / W] = make_float2(M, l);
+        p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + row] = make_float2(M, l);
       }
+      cm[lane % W * HP + row] = f;
+      __syncwarp();
 #pragma unroll 1
       for (int r0 = 0; r0 < rows; r0 += 32 / LR) {
         const int r = r0 + lane / LR;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float fw = __shfl_sync(0xffffffffu, f, min(W * r + w, 31));
+          const float fw = cm[w * HP + min(r, rows - 1)];
           const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + min(r, rows - 1)) * OP + d);
           a.x = fmaf(fw, v.x, a.x);
           a.y = fmaf(fw, v.y, a.y);
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
         for (uint32_t left = all; left != 0; left = __ballot_sync(0xffffffffu, todo)) {
           // (of a pending lane: a slot already sent to may be a phase further by now)
 #pragma unroll
-          for (int u = 0; u < 3; ++u) left = (left & (left - 1)) ? left & (left - 1) : left;
+          for (int u = 0; u < F::kGroup - 1; ++u) left = (left & (left - 1)) ? left & (left - 1) : left;
           const int at_lane = __ffs(left) - 1;
           // (a slot's first turn waits for the phase before the first, which counts as complete)
           ok = waitw(__shfl_sync(0xffffffffu, eb, at_lane), (__shfl_sync(0xffffffffu, turn, at_lane) - 1) & 1,

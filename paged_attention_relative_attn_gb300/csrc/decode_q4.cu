@@ -60,6 +60,7 @@ __device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32
 }
 
 struct Q4Format {
+  static constexpr int kGroup = 4;
   __host__ __device__ static constexpr int block_bytes(int D) { return q4_block_bytes(D); }
   // Rows 2t, 2t + 1 are keys t, 4 + (t ^ 1), so that the 64-byte rows read together lie in both halves
   // of the shared-memory banks, for K (rows 2t, 2t + 1 at once) and V (t = 0..3 at once).

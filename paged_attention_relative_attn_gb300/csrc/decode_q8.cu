@@ -42,6 +42,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 struct Q8Format {
+  static constexpr int kGroup = 1;  // a ring of 8 tiles (32 sequences to 32768 keys: 190.2 us; in fours 193.8)
   __host__ __device__ static constexpr int block_bytes(int D) { return q8_block_bytes(D); }
   __device__ static int key_of(int g) { return g; }
 
@@ -160,8 +161,9 @@ struct Q8Format {
         kf[u][0] = fminf(back[0] * s, kMostFactor);
         kf[u][1] = fminf(back[1] * s, kMostFactor);
         k_nan[u] = tail.y;
+        float odd[4];  // two chains of products (one: 32 sequences to 32768 keys 190.0 us instead of 187.6)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[u][x] = 0.f;
+        for (int x = 0; x < 4; ++x) sc[u][x] = odd[x] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
           // unit 4x + t of row g; in odd rows of 128 channels the halves x are exchanged
@@ -175,9 +177,12 @@ struct Q8Format {
             e4m3x4_to_f16(wl[i], a0, a2);
             e4m3x4_to_f16(wh[i], a1, a3);
             const uint4 q = qf[2 * x + (i >> 1)];
-            mma_f16(sc[u], a0, a1, a2, a3, (i & 1) ? q.z : q.x, (i & 1) ? q.w : q.y);
+            if (i & 1) mma_f16(odd, a0, a1, a2, a3, q.z, q.w);
+            else mma_f16(sc[u], a0, a1, a2, a3, q.x, q.y);
           }
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[u][x] += odd[x];
       }
     }
     __device__ __forceinline__ float score(const DecodeBlocksParams&, int u, int x, float raw, float bias,
