@@ -588,7 +588,112 @@ size_t inkling_rel_attn_prefill_q8_workspace_size(int32_t B, int32_t max_q_len,
                                                   int32_t max_seq_len);
 
 /*
- * inkling_rel_attn_packed -- one of the calls on the 4-bit and 8-bit caches and the tables,
+ * Shared pages
+ * ------------
+ * Requests with a common beginning (samples of one prompt) can own pages together.
+ * page_refs, int32 [num_pages], counts a page's owners beyond the first: 0 for a free
+ * page and for one that a single request holds, so inkling_rel_attn_build_tables, which
+ * hands out pages and knows nothing of owners, leaves it right.  Only full pages are
+ * shared; a request's last partial page is its own, so appends never write to a
+ * shared page as long as a request does not shrink below the tokens it shares.
+ * With forked requests, pages of ended ones go back by inkling_rel_attn_release_pages,
+ * before build_tables, which then gets their length as 0 (it would put
+ * a shared page on the stack).  The calls work on page ids: one set of tables serves
+ * every pool that it is for, bf16, 4-bit or 8-bit.  Results depend on the
+ * arguments alone, not on timing; B <= 8192 (0: nothing is written), page_size,
+ * page_table_stride, num_pages and the free stack as for build_tables.
+ */
+
+/*
+ * inkling_rel_attn_fork_pages -- requests that go on from another one's tokens.
+ * Row b with source[b] >= 0 gets the tokens of row source[b] as they are before the
+ * call: its full pages are shared (page_refs grows by 1 for each), and its last partial
+ * page, if it has one, becomes a page off the stack in row b, whose content
+ * inkling_rel_attn_copy_pages then copies in every pool.  Pages are taken from the
+ * top, in batch order; a row that needs one and finds none is refused
+ * (INKLING_DEVERR_NO_PAGES): it stays empty.  A row that holds tokens already, or whose
+ * source is not a row: INKLING_DEVERR_BAD_SLOT, left as it is.  A source longer than its
+ * row: INKLING_DEVERR_SEQ_TOO_LONG, the fork stays empty.
+ *
+ *   source        int32 [B]; -1: nothing to do
+ *   seq_lens      int32 [B], tokens held
+ *   page_table    int32 [B, page_table_stride], rows of forks written in place
+ *   page_refs     int32 [num_pages], updated in place
+ *   free_pages    int32 [num_pages], free_count int32 [1]: the stack, read
+ *   kv_lens       int32 [B], out: seq_lens, and the tokens of each fork.  May be seq_lens itself
+ *   copy_src, copy_dst int32 [B], out: the pages to copy for row b; -1: none
+ *   free_left     int32 [1], out: the stack's height.  May be free_count itself
+ */
+int inkling_rel_attn_fork_pages(
+    const int32_t* source, const int32_t* seq_lens, int32_t* page_table,
+    int32_t page_table_stride, int32_t* page_refs, const int32_t* free_pages,
+    const int32_t* free_count, int32_t B, int32_t page_size, int32_t num_pages,
+    int32_t* kv_lens, int32_t* copy_src, int32_t* copy_dst, int32_t* free_left,
+    int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_release_pages -- pages of ended requests (new_lens[b] < 0).  Every
+ * page of such a row loses an owner; one without owners goes on the stack: in batch
+ * order and each row in page order, a page that several of the rows owned at the last
+ * of them.  More rows than page_refs knows owners: INKLING_DEVERR_BAD_PAGE, the page
+ * goes back once.  A stack that would grow past num_pages:
+ * INKLING_DEVERR_BAD_PAGE, the pages past it are dropped.
+ *
+ *   seq_lens      int32 [B], tokens held; new_lens int32 [B], as for build_tables
+ *   page_table    int32 [B, page_table_stride], read
+ *   page_refs     int32 [num_pages], updated in place
+ *   free_pages    int32 [num_pages], returned pages written above the top; free_count int32 [1]
+ *   kv_lens       int32 [B], out: seq_lens, but 0 for the ended.  May be seq_lens itself
+ *   free_left     int32 [1], out: the stack's height.  May be free_count itself
+ */
+int inkling_rel_attn_release_pages(
+    const int32_t* seq_lens, const int32_t* new_lens, const int32_t* page_table,
+    int32_t page_table_stride, int32_t* page_refs, int32_t* free_pages,
+    const int32_t* free_count, int32_t B, int32_t page_size, int32_t num_pages,
+    int32_t* kv_lens, int32_t* free_left, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_compact_pages -- the pages in use brought together at the low end
+ * of the pool.  Of the pages that a row holds (live) or that are on the stack, the
+ * lowest n are to be the live ones, n being their number: live pages past them move to
+ * free ones among them, both taken in ascending order.  Tables and page_refs are
+ * renumbered, the stack is rewritten with the lowest page on top; the pages' content
+ * is moved by inkling_rel_attn_copy_pages with the list that the call makes, before
+ * anything is appended.  Pages that are neither live nor on the stack are left alone.  A
+ * live page that is on the stack too: INKLING_DEVERR_BAD_PAGE, it stays in use.
+ *
+ *   seq_lens      int32 [B], tokens held
+ *   page_table    int32 [B, page_table_stride], updated in place
+ *   page_refs     int32 [num_pages], updated in place, or NULL (no shared pages)
+ *   free_pages    int32 [num_pages], rewritten up to the height; free_count int32 [1]
+ *   move_src, move_dst int32 [num_pages], out: the moves, -1 behind them
+ *   moves         int32 [1], out: their number
+ *   num_pages     up to 524288
+ */
+int inkling_rel_attn_compact_pages(
+    const int32_t* seq_lens, int32_t* page_table, int32_t page_table_stride,
+    int32_t* page_refs, int32_t* free_pages, const int32_t* free_count,
+    int32_t B, int32_t page_size, int32_t num_pages, int32_t* move_src,
+    int32_t* move_dst, int32_t* moves, int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_copy_pages -- page src[i] copied to page dst[i] in every pool, for
+ * i < n (and i < *count, where that is given).  Negative ids: skipped; ids past the
+ * pool: INKLING_DEVERR_BAD_PAGE, skipped.  The dst pages of a call are distinct and
+ * none of them is a src page of another pair.
+ *
+ *   pools       HOST array of n_pools device pointers, each 16-byte aligned, to
+ *               num_pages pages of page_bytes bytes (a multiple of 16): K and V of
+ *               the layers with one kind of cache (or rows of a state pool)
+ *   src, dst    int32 [n] (device); count int32 [1] (device) or NULL
+ */
+int inkling_rel_attn_copy_pages(
+    void* const* pools, int32_t n_pools, int64_t page_bytes, int32_t num_pages,
+    const int32_t* src, const int32_t* dst, int32_t n, const int32_t* count,
+    int32_t* device_error, void* stream);
+
+/*
+ * inkling_rel_attn_packed -- one of the calls on the 4-bit and 8-bit caches, the tables and pages,
  * with its `count` arguments in an array of 64-bit words, in the call's order:
  * pointers and integers as they are, `scale` as the bits of a double, the stream
  * last (INKLING_PACKED_BUILD_TABLES: 16 words, or the 17 of the _step form).  For bindings in which converting two dozen arguments one by one takes as
@@ -604,6 +709,10 @@ size_t inkling_rel_attn_prefill_q8_workspace_size(int32_t B, int32_t max_q_len,
 #define INKLING_PACKED_KV_READ_Q8 6
 #define INKLING_PACKED_DECODE_Q8 7
 #define INKLING_PACKED_PREFILL_Q8 8
+#define INKLING_PACKED_FORK_PAGES 9
+#define INKLING_PACKED_RELEASE_PAGES 10
+#define INKLING_PACKED_COMPACT_PAGES 11
+#define INKLING_PACKED_COPY_PAGES 12
 int inkling_rel_attn_packed(int32_t call, const int64_t* args, int32_t count);
 
 /*

@@ -9,6 +9,8 @@ from .ops import (  # noqa: F401
     InklingError,
     build_tables,
     choose_splits,
+    compact_pages,
+    copy_pages,
     decode,
     decode_inputs,
     decode_multi,
@@ -18,6 +20,7 @@ from .ops import (  # noqa: F401
     decode_q8,
     decode_q8_workspace_bytes,
     decode_workspace_bytes,
+    fork_pages,
     kv_append,
     kv_append_q4,
     kv_append_q8,
@@ -30,10 +33,12 @@ from .ops import (  # noqa: F401
     prefill_q4_workspace_bytes,
     prefill_q8,
     prefill_q8_workspace_bytes,
+    release_pages,
 )
 
-__all__ = ["InklingError", "build_tables", "choose_splits", "decode", "decode_inputs", "decode_multi",
-           "decode_multi_workspace_bytes", "decode_q4", "decode_q4_workspace_bytes", "decode_q8",
-           "decode_q8_workspace_bytes", "decode_workspace_bytes", "kv_append", "kv_append_q4", "kv_append_q8",
-           "kv_conv_append", "kv_read_q4", "kv_read_q8", "prefill", "prefill_inputs", "prefill_q4",
-           "prefill_q4_workspace_bytes", "prefill_q8", "prefill_q8_workspace_bytes"]
+__all__ = ["InklingError", "build_tables", "choose_splits", "compact_pages", "copy_pages", "decode",
+           "decode_inputs", "decode_multi", "decode_multi_workspace_bytes", "decode_q4",
+           "decode_q4_workspace_bytes", "decode_q8", "decode_q8_workspace_bytes", "decode_workspace_bytes",
+           "fork_pages", "kv_append", "kv_append_q4", "kv_append_q8", "kv_conv_append", "kv_read_q4",
+           "kv_read_q8", "prefill", "prefill_inputs", "prefill_q4", "prefill_q4_workspace_bytes",
+           "prefill_q8", "prefill_q8_workspace_bytes", "release_pages"]

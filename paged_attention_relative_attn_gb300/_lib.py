@@ -38,6 +38,10 @@ EXPORTED = (
     "inkling_rel_attn_decode_q8_workspace_size",
     "inkling_rel_attn_prefill_q8",
     "inkling_rel_attn_prefill_q8_workspace_size",
+    "inkling_rel_attn_fork_pages",
+    "inkling_rel_attn_release_pages",
+    "inkling_rel_attn_compact_pages",
+    "inkling_rel_attn_copy_pages",
     "inkling_rel_attn_packed",
     "inkling_rel_attn_choose_splits",
     "inkling_rel_attn_decode_workspace_size",
@@ -111,6 +115,21 @@ _SIGS = {
         _i32, _i32, _i32, _f32, _i32,               # num_pages R window scale max_seq_len
         _p, _p, _p, _sz, _p, _p]),                  # out lse ws ws_bytes err stream
     "inkling_rel_attn_prefill_q4_workspace_size": (_sz, [_i32] * 6),
+    "inkling_rel_attn_fork_pages": (ctypes.c_int, [
+        _p, _p, _p, _i32, _p, _p, _p,               # source seq_lens page_table stride refs free count
+        _i32, _i32, _i32,                           # B page_size num_pages
+        _p, _p, _p, _p, _p, _p]),                   # kv_lens copy_src copy_dst free_left err stream
+    "inkling_rel_attn_release_pages": (ctypes.c_int, [
+        _p, _p, _p, _i32, _p, _p, _p,               # seq_lens new_lens page_table stride refs free count
+        _i32, _i32, _i32,                           # B page_size num_pages
+        _p, _p, _p, _p]),                           # kv_lens free_left err stream
+    "inkling_rel_attn_compact_pages": (ctypes.c_int, [
+        _p, _p, _i32, _p, _p, _p,                   # seq_lens page_table stride refs free count
+        _i32, _i32, _i32,                           # B page_size num_pages
+        _p, _p, _p, _p, _p]),                       # move_src move_dst moves err stream
+    "inkling_rel_attn_copy_pages": (ctypes.c_int, [
+        _p, _i32, ctypes.c_int64, _i32,             # pools n_pools page_bytes num_pages
+        _p, _p, _i32, _p, _p, _p]),                 # src dst n count err stream
     "inkling_rel_attn_packed": (ctypes.c_int, [_i32, ctypes.c_char_p, _i32]),  # call args count
     "inkling_rel_attn_choose_splits": (_i32, [_i32, _i32, _i32, _i32, _i32]),
     "inkling_rel_attn_decode_workspace_size": (_sz, [_i32] * 8),
@@ -162,6 +181,10 @@ PACKED = {
     "inkling_rel_attn_kv_read_q8": (6, _q("12q").pack, 12),
     "inkling_rel_attn_decode_q8": (7, _q("16qd6q").pack, 23),
     "inkling_rel_attn_prefill_q8": (8, _q("18qd7q").pack, 26),
+    "inkling_rel_attn_fork_pages": (9, _q("16q").pack, 16),
+    "inkling_rel_attn_release_pages": (10, _q("14q").pack, 14),
+    "inkling_rel_attn_compact_pages": (11, _q("14q").pack, 14),
+    "inkling_rel_attn_copy_pages": (12, _q("10q").pack, 10),
 }
 
 
@@ -344,6 +367,42 @@ def inkling_rel_attn_prefill_q8(q, cu_seqlens_q, k_cache, v_cache, page_table, p
 def inkling_rel_attn_prefill_q8_workspace_size(B, max_q_len, H_kv, D, window, max_seq_len):
     return load().inkling_rel_attn_prefill_q8_workspace_size(B, max_q_len, H_kv, D, window,
                                                              max_seq_len)
+
+
+def inkling_rel_attn_fork_pages(source, seq_lens, page_table, page_table_stride, page_refs, free_pages, free_count, B,
+                                page_size, num_pages, kv_lens, copy_src, copy_dst, free_left, device_error, stream):
+    return load().inkling_rel_attn_fork_pages(
+        _v(source), _v(seq_lens), _v(page_table), page_table_stride, _v(page_refs), _v(free_pages), _v(free_count), B,
+        page_size, num_pages, _v(kv_lens), _v(copy_src), _v(copy_dst), _v(free_left), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_release_pages(seq_lens, new_lens, page_table, page_table_stride, page_refs, free_pages,
+                                   free_count, B, page_size, num_pages, kv_lens, free_left, device_error, stream):
+    return load().inkling_rel_attn_release_pages(
+        _v(seq_lens), _v(new_lens), _v(page_table), page_table_stride, _v(page_refs), _v(free_pages), _v(free_count),
+        B, page_size, num_pages, _v(kv_lens), _v(free_left), _v(device_error), _v(stream))
+
+
+def inkling_rel_attn_compact_pages(seq_lens, page_table, page_table_stride, page_refs, free_pages, free_count, B,
+                                   page_size, num_pages, move_src, move_dst, moves, device_error, stream):
+    return load().inkling_rel_attn_compact_pages(
+        _v(seq_lens), _v(page_table), page_table_stride, _v(page_refs), _v(free_pages), _v(free_count), B, page_size,
+        num_pages, _v(move_src), _v(move_dst), _v(moves), _v(device_error), _v(stream))
+
+
+def pointers(addresses):
+    """A host array of device pointers, for ``pools`` of inkling_rel_attn_copy_pages."""
+    return (ctypes.c_void_p * len(addresses))(*addresses)
+
+
+def address_of(array):
+    return ctypes.addressof(array)
+
+
+def inkling_rel_attn_copy_pages(pools, n_pools, page_bytes, num_pages, src, dst, n, count, device_error, stream):
+    """``pools``: the address of a host array of device pointers, or one made by ``pointers``."""
+    return load().inkling_rel_attn_copy_pages(
+        pools, n_pools, page_bytes, num_pages, _v(src), _v(dst), n, _v(count), _v(device_error), _v(stream))
 
 
 def inkling_rel_attn_choose_splits(B, H_kv, window, max_seq_len, num_sms):

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libinkling_rel_attn.so")
 SOURCES = ["api.cu", "decode.cu", "decode_noalloc.cu", "prefill.cu", "selftest.cu", "kv_append.cu",
            "kv_conv.cu", "api_q4.cu", "q4_rows.cu", "decode_q4.cu", "api_q8.cu", "q8_rows.cu", "decode_q8.cu",
-           "tables.cu"]
+           "tables.cu", "api_pages.cu", "pages.cu"]
 HEADERS = ["ptx.cuh", "async.cuh", "internal.h", "launch.h", "tc.cuh", "plan.cuh", "q4.cuh", "q8.cuh", "expand.cuh",
            "decode_blocks.cuh", "api_blocks.h"]
 

@@ -214,6 +214,60 @@ int inkling_rel_attn_packed(int32_t call, const int64_t* a, int32_t count) {
       return prefill(q, cu, k, v, table, stride, seq_lens, rel, B, T, max_q_len, H_q, H_kv, D, page_size, num_pages, R,
                      window, scale, max_seq_len, out, lse, ws, ws_bytes, err, ptr());
     }
+    case INKLING_PACKED_FORK_PAGES: {
+      if (count != 16) return INKLING_ERR_ARG;
+      const int32_t *source = ci(), *seq_lens = ci();
+      int32_t* table = static_cast<int32_t*>(ptr());
+      const int32_t stride = i32();
+      int32_t* refs = static_cast<int32_t*>(ptr());
+      const int32_t *free_pages = ci(), *free_count = ci();
+      const int32_t B = i32(), page_size = i32(), num_pages = i32();
+      int32_t* out[5];
+      for (int32_t*& o : out) o = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_fork_pages(source, seq_lens, table, stride, refs, free_pages, free_count, B, page_size,
+                                         num_pages, out[0], out[1], out[2], out[3], out[4], ptr());
+    }
+    case INKLING_PACKED_RELEASE_PAGES: {
+      if (count != 14) return INKLING_ERR_ARG;
+      const int32_t *seq_lens = ci(), *new_lens = ci(), *table = ci();
+      const int32_t stride = i32();
+      int32_t *refs = static_cast<int32_t*>(ptr()), *free_pages = static_cast<int32_t*>(ptr());
+      const int32_t* free_count = ci();
+      const int32_t B = i32(), page_size = i32(), num_pages = i32();
+      int32_t* out[3];
+      for (int32_t*& o : out) o = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_release_pages(seq_lens, new_lens, table, stride, refs, free_pages, free_count, B,
+                                            page_size, num_pages, out[0], out[1], out[2], ptr());
+    }
+    case INKLING_PACKED_COMPACT_PAGES: {
+      if (count != 14) return INKLING_ERR_ARG;
+      const int32_t* seq_lens = ci();
+      int32_t* table = static_cast<int32_t*>(ptr());
+      const int32_t stride = i32();
+      int32_t *refs = static_cast<int32_t*>(ptr()), *free_pages = static_cast<int32_t*>(ptr());
+      const int32_t* free_count = ci();
+      const int32_t B = i32(), page_size = i32(), num_pages = i32();
+      int32_t* out[4];
+      for (int32_t*& o : out) o = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_compact_pages(seq_lens, table, stride, refs, free_pages, free_count, B, page_size,
+                                            num_pages, out[0], out[1], out[2], out[3], ptr());
+    }
+    case INKLING_PACKED_COPY_PAGES: {
+      if (count != 10) return INKLING_ERR_ARG;
+      void* const* pools = static_cast<void* const*>(ptr());
+      const int32_t n_pools = i32();
+      const int64_t page_bytes = a[at++];
+      const int32_t num_pages = i32();
+      const int32_t *src = ci(), *dst = ci();
+      const int32_t n = i32();
+      const int32_t* moves = ci();
+      int32_t* err = static_cast<int32_t*>(ptr());
+      if (!fits) return INKLING_ERR_ARG;
+      return inkling_rel_attn_copy_pages(pools, n_pools, page_bytes, num_pages, src, dst, n, moves, err, ptr());
+    }
   }
   return INKLING_ERR_ARG;
 }

@@ -178,6 +178,41 @@ struct TablesCall {
   cudaStream_t stream;
 };
 
+// Forking, releasing and moving together of pages (each call uses some of the fields).
+struct PagesCall {
+  const int32_t* source;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* page_table;
+  int32_t pt_stride;
+  int32_t* page_refs;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t B, P, num_pages;
+  int32_t* kv_lens;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* count;
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
+constexpr int32_t kCompactMaxPages = 1 << 19;  // of a pool that is compacted: 12 bytes of shared memory for 32
+
+struct CopyPagesCall {
+  void* const* pools;  // host array of device pointers
+  int32_t n_pools;
+  int64_t page_bytes;
+  int32_t num_pages;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t n;
+  const int32_t* count;  // or null: all n
+  int32_t sms;  // of the device
+  int32_t* dev_err;
+  cudaStream_t stream;
+};
+
 int launch_decode(const DecodeCall& c);        // returns INKLING_* code
 int launch_q4_rows(const RowsCall& c, bool append);
 int launch_q8_rows(const RowsCall& c, bool append);
@@ -186,6 +221,10 @@ int launch_q8_expand(const ExpandCall& c);
 int launch_decode_q4(const DecodeBlocksCall& c);
 int launch_decode_q8(const DecodeBlocksCall& c);
 int launch_build_tables(const TablesCall& c);
+int launch_fork_pages(const PagesCall& c);
+int launch_release_pages(const PagesCall& c);
+int launch_compact_pages(const PagesCall& c);
+int launch_copy_pages(const CopyPagesCall& c);
 // of decode over the 4-bit or 8-bit cache
 size_t decode_q4_workspace_bytes(int32_t B, int32_t QL, int32_t H_q, int32_t H_kv, int32_t D, int32_t sms);
 int launch_prefill(const PrefillCall& c);      // returns INKLING_* code

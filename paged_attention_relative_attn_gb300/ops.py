@@ -629,6 +629,147 @@ def prefill_q8(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
                            max_seq_len, max_q_len, out, lse, workspace, device_error, stream)
 
 
+# ---------------------------------------------------------------------------
+# Shared pages
+# ---------------------------------------------------------------------------
+
+def _ints(dev, *specs):
+    """Refuse the first (tensor, name, shape) that is not contiguous int32 of that shape on device ``dev``."""
+    for t, _, shape in specs:
+        if not (t.dtype is _I32 and t.get_device() == dev and t.is_contiguous() and t.shape == shape):
+            _refuse(dev, [(t, name, _I32, len(shape)) for t, name, shape in specs])
+
+
+def _on_stream(stream, t, call):
+    """``call()`` with ``stream`` as the current one: buffers made there are that stream's."""
+    _own_stream(stream, t)
+    with torch.cuda.stream(stream):
+        return call()
+
+
+def fork_pages(source, seq_lens, page_table, page_refs, free_pages, free_count, *, page_size, kv_lens=None,
+               copy_src=None, copy_dst=None, free_left=None, device_error=None, stream=None):
+    """Requests that go on from another one's tokens, its full pages shared.  See
+    inkling_rel_attn_fork_pages.
+
+    source [B] int32 (the row to go on from, -1: nothing to do; forks are empty rows);
+    seq_lens [B] int32; page_table [B, stride] and page_refs [num_pages] int32, updated in
+    place; free_pages [num_pages] int32, a stack of free_count [1] int32 pages.
+    Returns (kv_lens [B], copy_src [B], copy_dst [B], free_left [1]), int32; pass them to
+    avoid allocations.  kv_lens=seq_lens and free_left=free_count step the state in
+    place.  ``copy_pages(pools, copy_src, copy_dst)`` then copies the partial pages.
+    """
+    if stream is not None:
+        return _on_stream(stream, seq_lens, lambda: fork_pages(
+            source, seq_lens, page_table, page_refs, free_pages, free_count, page_size=page_size, kv_lens=kv_lens,
+            copy_src=copy_src, copy_dst=copy_dst, free_left=free_left, device_error=device_error))
+    B, n = seq_lens.numel(), free_pages.numel()
+    kv_lens = torch.empty_like(seq_lens) if kv_lens is None else kv_lens
+    copy_src = torch.empty_like(seq_lens) if copy_src is None else copy_src
+    copy_dst = torch.empty_like(seq_lens) if copy_dst is None else copy_dst
+    free_left = torch.empty_like(free_count) if free_left is None else free_left
+    dev = seq_lens.get_device()
+    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
+    _ints(dev, (seq_lens, "seq_lens", (B,)), (source, "source", (B,)), (page_table, "page_table", (B, stride)),
+          (page_refs, "page_refs", (n,)), (free_pages, "free_pages", (n,)), (free_count, "free_count", (1,)),
+          (kv_lens, "kv_lens", (B,)), (copy_src, "copy_src", (B,)), (copy_dst, "copy_dst", (B,)),
+          (free_left, "free_left", (1,)))
+    _launch("inkling_rel_attn_fork_pages", dev, None, source.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
+            stride, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B, page_size, n,
+            kv_lens.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), free_left.data_ptr(),
+            _error_word(device_error, dev))
+    if B == 0 and free_left.data_ptr() != free_count.data_ptr():  # nothing was launched
+        free_left.copy_(free_count)
+    return kv_lens, copy_src, copy_dst, free_left
+
+
+def release_pages(seq_lens, new_lens, page_table, page_refs, free_pages, free_count, *, page_size, kv_lens=None,
+                  free_left=None, device_error=None, stream=None):
+    """Pages of ended requests (new_lens < 0) lose an owner; those without one go back on the stack.  See
+    inkling_rel_attn_release_pages.
+
+    Arguments as for ``fork_pages``; free_pages is written above its top.  Returns
+    (kv_lens [B]: seq_lens, but 0 for the ended, free_left [1]), int32.
+    """
+    if stream is not None:
+        return _on_stream(stream, seq_lens, lambda: release_pages(
+            seq_lens, new_lens, page_table, page_refs, free_pages, free_count, page_size=page_size, kv_lens=kv_lens,
+            free_left=free_left, device_error=device_error))
+    B, n = seq_lens.numel(), free_pages.numel()
+    kv_lens = torch.empty_like(seq_lens) if kv_lens is None else kv_lens
+    free_left = torch.empty_like(free_count) if free_left is None else free_left
+    dev = seq_lens.get_device()
+    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
+    _ints(dev, (seq_lens, "seq_lens", (B,)), (new_lens, "new_lens", (B,)), (page_table, "page_table", (B, stride)),
+          (page_refs, "page_refs", (n,)), (free_pages, "free_pages", (n,)), (free_count, "free_count", (1,)),
+          (kv_lens, "kv_lens", (B,)), (free_left, "free_left", (1,)))
+    _launch("inkling_rel_attn_release_pages", dev, None, seq_lens.data_ptr(), new_lens.data_ptr(),
+            page_table.data_ptr(), stride, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
+            page_size, n, kv_lens.data_ptr(), free_left.data_ptr(), _error_word(device_error, dev))
+    if B == 0 and free_left.data_ptr() != free_count.data_ptr():  # nothing was launched
+        free_left.copy_(free_count)
+    return kv_lens, free_left
+
+
+def compact_pages(seq_lens, page_table, free_pages, free_count, *, page_size, page_refs=None, move_src=None,
+                  move_dst=None, moves=None, device_error=None, stream=None):
+    """The pages in use brought together at the low end of the pool.  See inkling_rel_attn_compact_pages.
+
+    page_table, free_pages (up to its height) and page_refs, if given, are updated in
+    place.  Returns (move_src [num_pages], move_dst [num_pages], moves [1]), int32;
+    ``copy_pages(pools, move_src, move_dst, count=moves)`` then moves the pages' content.
+    """
+    if stream is not None:
+        return _on_stream(stream, seq_lens, lambda: compact_pages(
+            seq_lens, page_table, free_pages, free_count, page_size=page_size, page_refs=page_refs, move_src=move_src,
+            move_dst=move_dst, moves=moves, device_error=device_error))
+    B, n = seq_lens.numel(), free_pages.numel()
+    move_src = torch.empty_like(free_pages) if move_src is None else move_src
+    move_dst = torch.empty_like(free_pages) if move_dst is None else move_dst
+    moves = torch.empty_like(free_count) if moves is None else moves
+    dev = seq_lens.get_device()
+    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
+    _ints(dev, (seq_lens, "seq_lens", (B,)), (page_table, "page_table", (B, stride)), (free_pages, "free_pages", (n,)),
+          (free_count, "free_count", (1,)), (move_src, "move_src", (n,)), (move_dst, "move_dst", (n,)),
+          (moves, "moves", (1,)))
+    if page_refs is not None:
+        _ints(dev, (page_refs, "page_refs", (n,)))
+    _launch("inkling_rel_attn_compact_pages", dev, None, seq_lens.data_ptr(), page_table.data_ptr(), stride,
+            0 if page_refs is None else page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
+            page_size, n, move_src.data_ptr(), move_dst.data_ptr(), moves.data_ptr(), _error_word(device_error, dev))
+    return move_src, move_dst, moves
+
+
+def copy_pages(pools, src, dst, *, count=None, device_error=None, stream=None):
+    """Page src[i] copied to page dst[i] in every pool (in place).  See inkling_rel_attn_copy_pages.
+
+    pools: tensors of any type with pages along dimension 0, the same number of pages of
+    the same size (K and V of the layers with one kind of cache, in bf16, 4 or 8
+    bits); src, dst [n] int32 (negative: skipped); count [1] int32: the pairs to copy,
+    all without it.
+    """
+    pools = list(pools)
+    if not pools:
+        return
+    first = pools[0]
+    if stream is not None:
+        _own_stream(stream, first)
+    dev, n = first.get_device(), src.numel()
+    page_bytes = first.nbytes // max(first.shape[0], 1) if first.dim() > 0 else 0
+    for i, t in enumerate(pools):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"pools[{i}]: must be contiguous and on the other pools' device")
+        if t.dim() < 1 or t.shape[0] != first.shape[0] or t.nbytes != first.nbytes:
+            raise ValueError(f"pools[{i}]: pages of another number or size than those of the first pool")
+    _ints(dev, (src, "src", (n,)), (dst, "dst", (n,)))
+    if count is not None:
+        _ints(dev, (count, "count", (1,)))
+    table = _lib.pointers([t.data_ptr() for t in pools])
+    _launch("inkling_rel_attn_copy_pages", dev, stream, _lib.address_of(table), len(pools), page_bytes, first.shape[0],
+            src.data_ptr(), dst.data_ptr(), n, 0 if count is None else count.data_ptr(),
+            _error_word(device_error, dev))
+
+
 def decode_inputs(inp, **kw):
     """``decode`` on a workloads.DecodeInputs-like object."""
     return decode(inp.q, inp.k_cache, inp.v_cache, inp.page_table, inp.seq_lens, inp.rel_logits,
