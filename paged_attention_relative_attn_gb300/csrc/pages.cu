@@ -369,9 +369,10 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
 // ---------------------------------------------------------------------------
 // Copy.
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVec = 4;                                    // 16-byte loads in flight per thread
-constexpr int kCopyChunk = kCopyThreads * kCopyVec * 16;       // bytes
-constexpr int kCopyPools = 256;                                // of a launch (its parameters)
+constexpr int kCopyVec = 4;                                  // 16-byte loads of a thread's step
+constexpr int kCopyStep = kCopyThreads * kCopyVec;           // 16-byte words of a block's step
+constexpr int kCopyChunk = 4 * kCopyStep * 16;               // bytes a block takes at once
+constexpr int kCopyPools = 256;                              // of a launch (its parameters)
 
 struct CopyParams {
   uint8_t* pools[kCopyPools];
@@ -383,6 +384,7 @@ struct CopyParams {
   int n_pools, n, num_pages, chunks;
 };
 
+// Each step's loads go out before the stores of the step before.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
   await_previous_kernel();
   const int pairs = p.count ? min(max(*p.count, 0), p.n) : p.n;
@@ -398,15 +400,25 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     const int pool = rest / p.chunks;
     const int64_t at = (int64_t)(rest - pool * p.chunks) * kCopyChunk;
     const int n = (int)min((int64_t)kCopyChunk, p.page_bytes - at) / 16;
-    const uint4* a = reinterpret_cast<const uint4*>(p.pools[pool] + from * p.page_bytes + at);
-    uint4* b = reinterpret_cast<uint4*>(p.pools[pool] + to * p.page_bytes + at);
-    uint4 v[kCopyVec];
+    const uint4* a = reinterpret_cast<const uint4*>(p.pools[pool] + from * p.page_bytes + at) + threadIdx.x;
+    uint4* b = reinterpret_cast<uint4*>(p.pools[pool] + to * p.page_bytes + at) + threadIdx.x;
+    uint4 v[2][kCopyVec];
+    auto load = [&](uint4 (&r)[kCopyVec], int k0) {
 #pragma unroll
-    for (int k = 0; k < kCopyVec; ++k)
-      if ((int)threadIdx.x + k * kCopyThreads < n) v[k] = a[threadIdx.x + k * kCopyThreads];
+      for (int k = 0; k < kCopyVec; ++k)
+        if ((int)threadIdx.x + k0 + k * kCopyThreads < n) r[k] = a[k0 + k * kCopyThreads];
+    };
+    auto store = [&](const uint4 (&r)[kCopyVec], int k0) {
 #pragma unroll
-    for (int k = 0; k < kCopyVec; ++k)
-      if ((int)threadIdx.x + k * kCopyThreads < n) b[threadIdx.x + k * kCopyThreads] = v[k];
+      for (int k = 0; k < kCopyVec; ++k)
+        if ((int)threadIdx.x + k0 + k * kCopyThreads < n) b[k0 + k * kCopyThreads] = r[k];
+    };
+    load(v[0], 0);
+#pragma unroll
+    for (int s = 0; s < kCopyChunk / 16 / kCopyStep; ++s) {
+      if (s + 1 < kCopyChunk / 16 / kCopyStep) load(v[(s + 1) & 1], (s + 1) * kCopyStep);
+      store(v[s & 1], s * kCopyStep);
+    }
   }
 }
 

@@ -633,11 +633,9 @@ def prefill_q8(q, cu_seqlens_q, k_cache, v_cache, page_table, seq_lens, rel_logi
 # Shared pages
 # ---------------------------------------------------------------------------
 
-def _ints(dev, *specs):
-    """Refuse the first (tensor, name, shape) that is not contiguous int32 of that shape on device ``dev``."""
-    for t, _, shape in specs:
-        if not (t.dtype is _I32 and t.get_device() == dev and t.is_contiguous() and t.shape == shape):
-            _refuse(dev, [(t, name, _I32, len(shape)) for t, name, shape in specs])
+def _refuse_ints(dev, **tensors):
+    """_refuse of int32 tensors; all are of rank 1 but page_table."""
+    _refuse(dev, [(t, name, _I32, 2 if name == "page_table" else 1) for name, t in tensors.items()])
 
 
 def _on_stream(stream, t, call):
@@ -669,13 +667,22 @@ def fork_pages(source, seq_lens, page_table, page_refs, free_pages, free_count, 
     copy_dst = torch.empty_like(seq_lens) if copy_dst is None else copy_dst
     free_left = torch.empty_like(free_count) if free_left is None else free_left
     dev = seq_lens.get_device()
-    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
-    _ints(dev, (seq_lens, "seq_lens", (B,)), (source, "source", (B,)), (page_table, "page_table", (B, stride)),
-          (page_refs, "page_refs", (n,)), (free_pages, "free_pages", (n,)), (free_count, "free_count", (1,)),
-          (kv_lens, "kv_lens", (B,)), (copy_src, "copy_src", (B,)), (copy_dst, "copy_dst", (B,)),
-          (free_left, "free_left", (1,)))
+    if not (seq_lens.dtype is source.dtype is page_table.dtype is page_refs.dtype is free_pages.dtype is free_count.dtype
+            is kv_lens.dtype is copy_src.dtype is copy_dst.dtype is free_left.dtype is _I32
+            and source.get_device() == page_table.get_device() == page_refs.get_device() == free_pages.get_device()
+            == free_count.get_device() == kv_lens.get_device() == copy_src.get_device() == copy_dst.get_device()
+            == free_left.get_device() == dev
+            and seq_lens.is_contiguous() and source.is_contiguous() and page_table.is_contiguous()
+            and page_refs.is_contiguous() and free_pages.is_contiguous() and kv_lens.is_contiguous()
+            and copy_src.is_contiguous() and copy_dst.is_contiguous()
+            and seq_lens.dim() == free_pages.dim() == 1 and page_table.dim() == 2 and page_table.shape[0] == B
+            and source.shape == kv_lens.shape == copy_src.shape == copy_dst.shape == seq_lens.shape
+            and page_refs.shape == free_pages.shape and free_count.shape == free_left.shape == (1,)):
+        _refuse_ints(dev, seq_lens=seq_lens, source=source, page_table=page_table, page_refs=page_refs,
+                     free_pages=free_pages, free_count=free_count, kv_lens=kv_lens, copy_src=copy_src,
+                     copy_dst=copy_dst, free_left=free_left)
     _launch("inkling_rel_attn_fork_pages", dev, None, source.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
-            stride, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B, page_size, n,
+            page_table.shape[1], page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B, page_size, n,
             kv_lens.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), free_left.data_ptr(),
             _error_word(device_error, dev))
     if B == 0 and free_left.data_ptr() != free_count.data_ptr():  # nothing was launched
@@ -699,13 +706,20 @@ def release_pages(seq_lens, new_lens, page_table, page_refs, free_pages, free_co
     kv_lens = torch.empty_like(seq_lens) if kv_lens is None else kv_lens
     free_left = torch.empty_like(free_count) if free_left is None else free_left
     dev = seq_lens.get_device()
-    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
-    _ints(dev, (seq_lens, "seq_lens", (B,)), (new_lens, "new_lens", (B,)), (page_table, "page_table", (B, stride)),
-          (page_refs, "page_refs", (n,)), (free_pages, "free_pages", (n,)), (free_count, "free_count", (1,)),
-          (kv_lens, "kv_lens", (B,)), (free_left, "free_left", (1,)))
+    if not (seq_lens.dtype is new_lens.dtype is page_table.dtype is page_refs.dtype is free_pages.dtype
+            is free_count.dtype is kv_lens.dtype is free_left.dtype is _I32
+            and new_lens.get_device() == page_table.get_device() == page_refs.get_device() == free_pages.get_device()
+            == free_count.get_device() == kv_lens.get_device() == free_left.get_device() == dev
+            and seq_lens.is_contiguous() and new_lens.is_contiguous() and page_table.is_contiguous()
+            and page_refs.is_contiguous() and free_pages.is_contiguous() and kv_lens.is_contiguous()
+            and seq_lens.dim() == free_pages.dim() == 1 and page_table.dim() == 2 and page_table.shape[0] == B
+            and new_lens.shape == kv_lens.shape == seq_lens.shape and page_refs.shape == free_pages.shape
+            and free_count.shape == free_left.shape == (1,)):
+        _refuse_ints(dev, seq_lens=seq_lens, new_lens=new_lens, page_table=page_table, page_refs=page_refs,
+                     free_pages=free_pages, free_count=free_count, kv_lens=kv_lens, free_left=free_left)
     _launch("inkling_rel_attn_release_pages", dev, None, seq_lens.data_ptr(), new_lens.data_ptr(),
-            page_table.data_ptr(), stride, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
-            page_size, n, kv_lens.data_ptr(), free_left.data_ptr(), _error_word(device_error, dev))
+            page_table.data_ptr(), page_table.shape[1], page_refs.data_ptr(), free_pages.data_ptr(),
+            free_count.data_ptr(), B, page_size, n, kv_lens.data_ptr(), free_left.data_ptr(), _error_word(device_error, dev))
     if B == 0 and free_left.data_ptr() != free_count.data_ptr():  # nothing was launched
         free_left.copy_(free_count)
     return kv_lens, free_left
@@ -728,13 +742,19 @@ def compact_pages(seq_lens, page_table, free_pages, free_count, *, page_size, pa
     move_dst = torch.empty_like(free_pages) if move_dst is None else move_dst
     moves = torch.empty_like(free_count) if moves is None else moves
     dev = seq_lens.get_device()
-    stride = page_table.shape[-1] if page_table.dim() == 2 else 0
-    _ints(dev, (seq_lens, "seq_lens", (B,)), (page_table, "page_table", (B, stride)), (free_pages, "free_pages", (n,)),
-          (free_count, "free_count", (1,)), (move_src, "move_src", (n,)), (move_dst, "move_dst", (n,)),
-          (moves, "moves", (1,)))
-    if page_refs is not None:
-        _ints(dev, (page_refs, "page_refs", (n,)))
-    _launch("inkling_rel_attn_compact_pages", dev, None, seq_lens.data_ptr(), page_table.data_ptr(), stride,
+    refs = free_pages if page_refs is None else page_refs  # (checked alike)
+    if not (seq_lens.dtype is page_table.dtype is free_pages.dtype is free_count.dtype is move_src.dtype
+            is move_dst.dtype is moves.dtype is refs.dtype is _I32
+            and page_table.get_device() == free_pages.get_device() == free_count.get_device() == move_src.get_device()
+            == move_dst.get_device() == moves.get_device() == refs.get_device() == dev
+            and seq_lens.is_contiguous() and page_table.is_contiguous() and free_pages.is_contiguous()
+            and move_src.is_contiguous() and move_dst.is_contiguous() and refs.is_contiguous()
+            and seq_lens.dim() == free_pages.dim() == 1 and page_table.dim() == 2 and page_table.shape[0] == B
+            and move_src.shape == move_dst.shape == refs.shape == free_pages.shape
+            and free_count.shape == moves.shape == (1,)):
+        _refuse_ints(dev, seq_lens=seq_lens, page_table=page_table, free_pages=free_pages, free_count=free_count,
+                     page_refs=refs, move_src=move_src, move_dst=move_dst, moves=moves)
+    _launch("inkling_rel_attn_compact_pages", dev, None, seq_lens.data_ptr(), page_table.data_ptr(), page_table.shape[1],
             0 if page_refs is None else page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
             page_size, n, move_src.data_ptr(), move_dst.data_ptr(), moves.data_ptr(), _error_word(device_error, dev))
     return move_src, move_dst, moves
@@ -743,29 +763,30 @@ def compact_pages(seq_lens, page_table, free_pages, free_count, *, page_size, pa
 def copy_pages(pools, src, dst, *, count=None, device_error=None, stream=None):
     """Page src[i] copied to page dst[i] in every pool (in place).  See inkling_rel_attn_copy_pages.
 
-    pools: tensors of any type with pages along dimension 0, the same number of pages of
+    pools: a list of tensors of any type with pages along dimension 0, the same number of pages of
     the same size (K and V of the layers with one kind of cache, in bf16, 4 or 8
     bits); src, dst [n] int32 (negative: skipped); count [1] int32: the pairs to copy,
     all without it.
     """
-    pools = list(pools)
     if not pools:
         return
     first = pools[0]
     if stream is not None:
         _own_stream(stream, first)
-    dev, n = first.get_device(), src.numel()
-    page_bytes = first.nbytes // max(first.shape[0], 1) if first.dim() > 0 else 0
+    dev, n, size = first.get_device(), src.numel(), first.nbytes
+    pages = first.shape[0] if first.dim() > 0 else 0
     for i, t in enumerate(pools):
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"pools[{i}]: must be contiguous and on the other pools' device")
-        if t.dim() < 1 or t.shape[0] != first.shape[0] or t.nbytes != first.nbytes:
+        if t.nbytes != size or t.dim() < 1 or t.shape[0] != pages:
             raise ValueError(f"pools[{i}]: pages of another number or size than those of the first pool")
-    _ints(dev, (src, "src", (n,)), (dst, "dst", (n,)))
-    if count is not None:
-        _ints(dev, (count, "count", (1,)))
+    if not (src.dtype is dst.dtype is _I32 and src.get_device() == dst.get_device() == dev and src.is_contiguous()
+            and dst.is_contiguous() and src.dim() == 1 and src.shape == dst.shape):
+        _refuse_ints(dev, src=src, dst=dst)
+    if count is not None and not (count.dtype is _I32 and count.get_device() == dev and count.shape == (1,)):
+        _refuse_ints(dev, count=count)
     table = _lib.pointers([t.data_ptr() for t in pools])
-    _launch("inkling_rel_attn_copy_pages", dev, stream, _lib.address_of(table), len(pools), page_bytes, first.shape[0],
+    _launch("inkling_rel_attn_copy_pages", dev, stream, _lib.address_of(table), len(pools), size // max(pages, 1), pages,
             src.data_ptr(), dst.data_ptr(), n, 0 if count is None else count.data_ptr(),
             _error_word(device_error, dev))
 
