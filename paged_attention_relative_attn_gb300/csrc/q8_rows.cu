@@ -9,11 +9,13 @@
 // Append.  What is written together is a block: its exponent comes from all of its
 // rows.  The tokens that join a block lie within 16 of the call; the first of them
 // leads.  A warp looks at a window of tokens, the 16 before and the 16 behind it (two
-// loads), and for each leader in the window takes its tokens' rows of one KV head, K
-// and V: the rows into registers (16 bytes a lane), their largest magnitude by one
+// loads), and for each leader in the window takes its tokens' rows of one KV head of K
+// or V: the rows into registers (16 bytes a lane), their largest magnitude by one
 // reduction, the block's scale as it was, and out go 8 bytes a lane.  Nothing but the
 // one warp touches a block, so no atomic is needed and the result does not depend on
 // timing.  Rows that the block has already are read only when its exponent grows.
+// 8192 tokens x 16 heads, D = 128: 20.8 us for 101 MB, 0.71 of the measured copy rate (K
+// and V by one warp, which then holds twice the registers: 24.0).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -96,15 +98,15 @@ __device__ __forceinline__ void q8_join(uint8_t* blk, const uint4 (&raw)[D / 16]
     *reinterpret_cast<uint4*>(blk + q8_tail_off(D)) = make_uint4(q8_scale_bits(e), flags, 0u, 0u);
 }
 
+constexpr int kAppendThreads = 128;
+
 // WIN: tokens whose leaders a warp looks after.
-template <int D, int WIN>
-__global__ void __launch_bounds__(kRowThreads)
-    kv_append_q8_kernel(const __grid_constant__ Q8RowsParams p) {
-  await_previous_kernel();
+template <int D, int WIN, bool IS_V>
+__device__ __forceinline__ void append_side(const Q8RowsParams& p, const uint4* rows, uint8_t* cache) {
   constexpr int U = D / 8, RP = 32 / U, N = 16 / RP;
   static_assert(N == D / 16, "steps of a block");
   const int lane = threadIdx.x & 31, h = blockIdx.y;
-  const int64_t t0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * WIN;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5)) * WIN;
   if (t0 >= p.T) return;
   // blocks of the 32 tokens that end with the window, and slots of the 32 that begin with it
   auto slot_of = [&](int64_t t, bool tell) {
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     return s;
   };
-  const int64_t back = slot_of(t0 + WIN - 32 + lane, false), slot = slot_of(t0 + lane, lane < WIN && h == 0);
+  const int64_t back = slot_of(t0 + WIN - 32 + lane, false), slot = slot_of(t0 + lane, lane < WIN && h == 0 && !IS_V);
   // (a skipped token's slot is negative, and so is this number of its block)
   const uint32_t alike = __match_any_sync(0xffffffffu, back >> 4);
   uint32_t leaders = __ballot_sync(0xffffffffu, lane >= 32 - WIN && back >= 0 && __ffs(alike) - 1 == lane);
@@ -128,24 +130,29 @@ __global__ void __launch_bounds__(kRowThreads)
     const bool dense = (run & behind) == 0u;  // next to each other
     const int len = min(__popc(run), kQ8Block);
     const uint32_t joins = __reduce_or_sync(0xffffffffu, (run >> lane) & 1u ? 1u << (slot & 15) : 0u);
-    uint4 kr[N], vr[N];
+    uint4 raw[N];
     int place[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int k = RP * i + lane / U;
       const int at_lane = k >= len ? l : dense ? l + k : (int)__fns(run, 0, k + 1);
       place[i] = (int)__shfl_sync(0xffffffffu, (int)(slot & 15), at_lane);
-      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      raw[i] = make_uint4(0, 0, 0, 0);
       if (k < len) {
         const size_t at = ((size_t)(t0 + at_lane) * p.H_kv + h) * U + lane % U;
-        kr[i] = __ldcs(p.k_rows + at);
-        vr[i] = __ldcs(p.v_rows + at);
+        raw[i] = __ldcs(rows + at);
       }
     }
-    const size_t at = q8_slot_at(p, first, h, D);
-    q8_join<D, false>(p.k_cache + at, kr, place, len, joins);
-    q8_join<D, true>(p.v_cache + at, vr, place, len, joins);
+    q8_join<D, IS_V>(cache + q8_slot_at(p, first, h, D), raw, place, len, joins);
   }
+}
+
+template <int D, int WIN>
+__global__ void __launch_bounds__(kAppendThreads)
+    kv_append_q8_kernel(const __grid_constant__ Q8RowsParams p) {
+  await_previous_kernel();
+  if (blockIdx.z == 0) append_side<D, WIN, false>(p, p.k_rows, p.k_cache);
+  else append_side<D, WIN, true>(p, p.v_rows, p.v_cache);
 }
 
 // The 8 K and 8 V channels of unit u of row r of the blocks at kb, vb, as bf16; zeros without a block.
@@ -171,42 +178,62 @@ struct Q8ReadFormat {
   }
 };
 
-template <int D>
+constexpr int kReadHeads = 2;  // of a large call (8192 tokens x 16 heads, D = 128: 17.6 us; 1: 18.4, 4: 19.8)
+
+// HEADS: heads per thread, which share the token's place in the cache.
+template <int D, int HEADS>
 __global__ void __launch_bounds__(kRowThreads)
     kv_read_q8_kernel(const __grid_constant__ Q8RowsParams p) {
   await_previous_kernel();
   constexpr int U = D / 8;
   const int64_t t_row = (int64_t)blockIdx.x * (kRowThreads / U) + threadIdx.x / U;
-  const int h = blockIdx.y, u = threadIdx.x % U;
+  const int h0 = blockIdx.y * HEADS, u = threadIdx.x % U;
   if (t_row >= p.T) return;
   int64_t slot = p.slots[t_row];
   if (slot >= (int64_t)p.num_pages * p.P) {
     report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
     slot = -1;
   }
-  const size_t at = slot >= 0 ? q8_slot_at(p, slot, h, D) : 0;
-  uint4 k, v;
-  Q8ReadFormat::read8<D>(p.k_cache + at, p.v_cache + at, slot >= 0, (int)(slot & 15), u, k, v);
-  const size_t to = ((size_t)t_row * p.H_kv + h) * U + u;
-  p.k_rows[to] = k;
-  p.v_rows[to] = v;
+  const size_t at = slot >= 0 ? q8_slot_at(p, slot, h0, D) : 0;
+  const size_t head = (size_t)(p.P / kQ8Block) * q8_block_bytes(D);  // from a head's block to the next head's
+  uint4 k[HEADS], v[HEADS];
+#pragma unroll
+  for (int x = 0; x < HEADS; ++x)
+    Q8ReadFormat::read8<D>(p.k_cache + at + x * head, p.v_cache + at + x * head, slot >= 0 && h0 + x < p.H_kv,
+                           (int)(slot & 15), u, k[x], v[x]);
+#pragma unroll
+  for (int x = 0; x < HEADS; ++x) {
+    if (h0 + x >= p.H_kv) return;
+    const size_t to = ((size_t)t_row * p.H_kv + h0 + x) * U + u;
+    p.k_rows[to] = k[x];
+    p.v_rows[to] = v[x];
+  }
 }
 
 template <int D>
 static bool rows_launch(const Q8RowsParams& p, bool append, cudaStream_t stream) {
   if (!append) {
     constexpr int kTokens = kRowThreads / (D / 8);
-    const dim3 g((unsigned)(((int64_t)p.T + kTokens - 1) / kTokens), (unsigned)p.H_kv);
-    return launch_dependent(kv_read_q8_kernel<D>, g, kRowThreads, 0, p, stream);
+    // one head and two, D = 128: 16384 rows 4.0 and 4.2 us, 32768: 6.1 and 6.0; 40960 of D = 64: 4.6 and 5.2
+    const bool many = (int64_t)p.T * p.H_kv * (D / 8) >= 32768 * 16;
+    const int heads = many ? kReadHeads : 1;
+    const dim3 g((unsigned)(((int64_t)p.T + kTokens - 1) / kTokens), (unsigned)((p.H_kv + heads - 1) / heads));
+    return many ? launch_dependent(kv_read_q8_kernel<D, kReadHeads>, g, kRowThreads, 0, p, stream)
+                : launch_dependent(kv_read_q8_kernel<D, 1>, g, kRowThreads, 0, p, stream);
   }
-  constexpr int kWarps = kRowThreads / 32;
+  constexpr int kWarps = kAppendThreads / 32;
   auto grid = [&](int win) {
     const int64_t windows = ((int64_t)p.T + win - 1) / win;
-    return dim3((unsigned)((windows + kWarps - 1) / kWarps), (unsigned)p.H_kv);
+    return dim3((unsigned)((windows + kWarps - 1) / kWarps), (unsigned)p.H_kv, 2);
   };
-  const bool many = (int64_t)p.T * p.H_kv >= 16384;
-  return many ? launch_dependent(kv_append_q8_kernel<D, 16>, grid(16), kRowThreads, 0, p, stream)
-              : launch_dependent(kv_append_q8_kernel<D, 1>, grid(1), kRowThreads, 0, p, stream);
+  // Wide windows leave few warps without a block of their own, but take single tokens, as a decode
+  // step's are, one after the other.  us with windows of 1, 4, 8 tokens (152 SMs, D = 128): 512
+  // (token, head) pairs of single tokens 3.0, 5.6, 9.8; 2048: 5.0, 7.1, 10.2; 8192: 16.2, 12.1, 16.1; of runs of
+  // tokens 2048: 3.5, 3.0, 2.8; 8192: 6.4, 4.0, 4.0; 16384: 10.4, 6.4, 5.0; 131072: -, 24.4, 20.8.
+  const int64_t pairs = (int64_t)p.T * p.H_kv;
+  return pairs >= 16384  ? launch_dependent(kv_append_q8_kernel<D, 8>, grid(8), kAppendThreads, 0, p, stream)
+         : pairs >= 4096 ? launch_dependent(kv_append_q8_kernel<D, 4>, grid(4), kAppendThreads, 0, p, stream)
+                         : launch_dependent(kv_append_q8_kernel<D, 1>, grid(1), kAppendThreads, 0, p, stream);
 }
 
 int launch_q8_rows(const RowsCall& c, bool append) {
