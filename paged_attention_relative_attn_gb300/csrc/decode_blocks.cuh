@@ -83,6 +83,7 @@ struct DecodeBlocksParams {
   int HI, HG;  // query heads of a KV head per item, items for all of them
   int NT, NR;  // token groups of a sequence; rows of an item at most
   int inv_G;   // 256 / G, rounded up (items of several tokens have all G <= 4 heads): rows divide by a product
+  uint32_t inv_P;      // 2^32 / P, rounded up
   int slots;           // ring slots
   int bias_prefetch;   // rel_logits rows are 16-byte aligned
   float scale;         // what the format multiplies its products by
@@ -147,13 +148,26 @@ __device__ __forceinline__ GroupRange group_range(const DecodeBlocksParams& p, i
 __device__ __forceinline__ int clamped_len(const DecodeBlocksParams& p, int b) {
   return min(max(p.seq_lens[b], 0), p.pt_stride * p.P);
 }
-// Tiles of one KV head of sequence b (all its items); 0 when it has fewer keys than new tokens.
-__device__ __forceinline__ int head_tiles(const DecodeBlocksParams& p, int b) {
-  const int L = clamped_len(p, b);
+// Tiles of one KV head of a sequence of length L (all its items); 0 when it has fewer keys than new tokens.
+__device__ __forceinline__ int head_tiles(const DecodeBlocksParams& p, int L) {
   if (L < p.QL) return 0;
   int n = 0;
   for (int tg = 0; tg < p.NT; ++tg) n += group_range(p, L, tg).ntile;
   return n * p.HG;
+}
+
+// Numbers of tiles nearly always fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ int64_t div_tiles(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// Page and place of a key.  The product with 2^32 / P rounded up is at most one too large.
+__device__ __forceinline__ int2 page_place(const DecodeBlocksParams& p, int key) {
+  int q = (int)__umulhi((uint32_t)key, p.inv_P), r = key - q * p.P;
+  if (r < 0) {
+    --q;
+    r += p.P;
+  }
+  return make_int2(q, r);
 }
 
 // MULTI: items of several tokens, so rows of several positions.
@@ -215,32 +229,49 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
   // Both walk the run: warp W sends the tiles, warp W + 1 prepares the items.
   if (warp >= W) {
     const bool copier = warp == W;
-    // ---- this thread block's run [x, x1) of the batch's tiles
-    int64_t total = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      total += (int64_t)p.H_kv * head_tiles(p, b);
-      if (copier && blockIdx.x == 0) {
-        const int Lr = p.seq_lens[b];
-        if (Lr > p.pt_stride * p.P) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
-        if (p.QL > 1 && Lr < p.QL) report(p.dev_err, INKLING_DEVERR_BAD_CHUNK);
+    // ---- this thread block's run [x, x1) of the batch's tiles.  A lane has four sequences
+    // of 128, whose lengths are asked for together; up to 128 are read once.
+    int tiles[4];  // of one KV head
+    auto read = [&](int b0, bool tell) {
+      int len[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int b = b0 + 4 * lane + k;
+        len[k] = b < p.B ? p.seq_lens[b] : -1;
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int cap = p.pt_stride * p.P;
+        tiles[k] = head_tiles(p, min(len[k], cap));
+        if (tell && b0 + 4 * lane + k < p.B) {
+          if (len[k] > cap) report(p.dev_err, INKLING_DEVERR_SEQ_TOO_LONG);
+          if (p.QL > 1 && len[k] < p.QL) report(p.dev_err, INKLING_DEVERR_BAD_CHUNK);
+        }
+      }
+      return (int64_t)p.H_kv * ((int64_t)tiles[0] + tiles[1] + tiles[2] + tiles[3]);
+    };
+    int64_t total = 0, mine = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 128) {
+      mine = read(b0, copier && blockIdx.x == 0);
+      total += mine;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     const int64_t runs = min((int64_t)gridDim.x, max((total + kRunMinRun - 1) / kRunMinRun, (int64_t)1));
     int64_t x = total, x1 = total;
-    if (blockIdx.x < runs) {
-      x = total * blockIdx.x / runs;
-      x1 = total * (blockIdx.x + 1) / runs;
+    if (blockIdx.x < runs) {  // total * i / runs, rounded down
+      const int64_t each = div_tiles(total, runs);
+      const uint32_t left = (uint32_t)(total - each * runs), r = (uint32_t)runs, i = blockIdx.x;
+      x = each * i + left * i / r;
+      x1 = each * (i + 1) + left * (i + 1) / r;
     }
     // ---- the item at x
-    int b = 0, hkv = 0, tg = 0, hg = 0, nb = 0, off = 0, L = 0;  // nb: tiles per head of sequence b
+    int b = 0, hkv = 0, tg = 0, hg = 0, off = 0, L = 0;
     if (x < x1) {
       int64_t carry = 0;
-      for (int b0 = 0;; b0 += 32) {
-        const int bb = b0 + lane;
-        const int mine = bb < p.B ? head_tiles(p, bb) : 0;
-        int64_t incl = (int64_t)p.H_kv * mine;
+      for (int b0 = 0;; b0 += 128) {
+        if (p.B > 128) mine = read(b0, false);
+        int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -249,10 +280,17 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
         const uint32_t past = __ballot_sync(0xffffffffu, carry + incl > x);
         if (past) {
           const int src = __ffs(past) - 1;
-          b = b0 + src;
-          nb = __shfl_sync(0xffffffffu, mine, src);
-          const int64_t at = x - (carry + __shfl_sync(0xffffffffu, incl, src) - (int64_t)p.H_kv * nb);
-          hkv = (int)(at / nb);
+          int64_t at = x - (carry + __shfl_sync(0xffffffffu, incl - mine, src));
+          int nb = 0;  // tiles per head of sequence b
+          b = b0 + 4 * src;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            nb = __shfl_sync(0xffffffffu, tiles[k], src);
+            if (at < (int64_t)p.H_kv * nb) break;
+            at -= (int64_t)p.H_kv * nb;
+            ++b;
+          }
+          hkv = (int)div_tiles(at, nb);
           off = (int)(at - (int64_t)hkv * nb);
           break;
         }
@@ -386,7 +424,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
         it.part = off > 0 ? 0 : 1;
         if (off == 0) {  // the thread block with an item's first part has the record of its cut
           const int64_t e = x + r.ntile - 1;
-          const int last = (int)(((e + 1) * runs - 1) / total);
+          const int last = (int)div_tiles((e + 1) * runs - 1, total);
           cut = make_int4(it.row0, it.tn, last - (int)blockIdx.x + 1, it.heads);
         }
       }
@@ -414,7 +452,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
       auto seen = [&](int key, int u) { return u == 0 ? key >= before : key <= pos1; };
       auto page_of = [&](int i, int u) -> int {  // page of block u of tile i; -1: not seen
         const int key = (it.tile0 + i) * TK + 16 * u;
-        return copier && lane < batch && i < it.ntile && seen(key, u) ? pt_row[key / p.P] : -1;
+        return copier && lane < batch && i < it.ntile && seen(key, u) ? pt_row[page_place(p, key).x] : -1;
       };
       int page[U], next[U];
 #pragma unroll
@@ -429,7 +467,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
           page[u] = next[u];
           next[u] = page_of(i + batch, u);
           fine[u] = page[u] >= 0 && page[u] < p.num_pages;
-          place[u] = (key0 + 16 * u) % p.P;
+          place[u] = page_place(p, key0 + 16 * u).y;
         }
         bool todo = lane < batch && i < it.ntile;
         const uint32_t all = __ballot_sync(0xffffffffu, todo);
@@ -819,6 +857,7 @@ inline DecodeBlocksParams run_params(const DecodeBlocksCall& c, const RunPlan& p
   p.HG = plan.HG;
   p.NT = plan.NT;
   p.inv_G = 255 / plan.G + 1;
+  p.inv_P = (uint32_t)(0xffffffffu / (uint32_t)c.P) + 1;
   p.NR = plan.NR;
   p.bias_prefetch = c.R % 4 == 0 && (reinterpret_cast<uintptr_t>(c.rel) & 15) == 0;
   return p;
