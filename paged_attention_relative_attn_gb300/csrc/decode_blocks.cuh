@@ -19,7 +19,7 @@
 // contiguous) into a ring of slots by bulk copy, a lane per tile; the ring runs
 // across items, so the next one streams in while the current one is finished.  The
 // other prepares the items (q as operands, bias pointers and positions per lane),
-// three ahead.  Consumer warp w takes the ring's tiles w, w + 4, ... with an online
+// three ahead; the 8-bit cache has a third for the sums of items of several tokens.  Consumer warp w takes the ring's tiles w, w + 4, ... with an online
 // softmax of its own; at the item's end it leaves (m, l, O) in one of two
 // shared-memory buffers and goes on, and the preparing warp adds the parts up.  (One
 // producer, and the last consumer to leave its part adding them up: over the 4-bit
@@ -35,6 +35,7 @@
 //   zero_block       a block that reads as zeros, at two places of shared memory (K, V)
 //   prepare          q of an item's rows as operands, and up to 4 words beside (RunPrep::extra)
 //   kGroup           tiles whose copies go out together (those of a long ring)
+//   kJoiner          whether a third producer warp fits the registers
 //   Consumer         the products S^T = K Q^T (16 keys x rows) and O^T += V^T P^T of a warp
 #pragma once
 
@@ -58,7 +59,17 @@ constexpr int kRunSmemPerSm = 222 * 1024;
 constexpr float kRunSlack = 5.5f;     // scores may exceed the exponent base by e^5.5 before it moves
 constexpr int kRunW = 4;              // consumer warps
 constexpr int kRunCtas = 2;           // thread blocks per SM
-constexpr int kRunThreads = 32 * (kRunW + 2);
+// Items of several tokens have up to 8 rows to add up, a warp's work of its own where the registers
+// allow it (8-bit, 64 sequences of 4 drafts: 57.3 us, by the preparing warp 62.5; items of one token,
+// with 3 rows, 36.6 and 35.7).
+template <class F, bool MULTI>
+constexpr bool run_joiner() {
+  return F::kJoiner && MULTI;
+}
+template <class F, bool MULTI>
+constexpr int run_threads() {
+  return 32 * (kRunW + (run_joiner<F, MULTI>() ? 3 : 2));
+}
 constexpr int kRunMergeWarps = 4;     // of the joining kernel's blocks: a thread per channel in all
 constexpr int kRunU = 2;              // 16-token blocks per tile
 constexpr int kRunTile = 16 * kRunU;  // keys per tile
@@ -175,11 +186,12 @@ __device__ __forceinline__ int2 page_place(const DecodeBlocksParams& p, int key)
 // instead of 55.2 for 64 sequences of 4 drafts over the 4-bit cache, the compiler having
 // treated the parameters as memory before it inlined.)
 template <class F, int D, bool MULTI>
-__global__ void __launch_bounds__(kRunThreads, kRunCtas)
+__global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
     decode_blocks_kernel(const __grid_constant__ DecodeBlocksParams p) {
   constexpr int W = kRunW, U = kRunU, TK = kRunTile;
   constexpr int HP = kRunRows;
   constexpr int OP = D + 4;
+  constexpr bool JOINER = run_joiner<F, MULTI>();
   constexpr int BLK = F::block_bytes(D);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -206,14 +218,14 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
   };
   const int key_g = F::key_of(g);  // key of a block that MMA row g stands for (and g + 8: 8 more)
 
-  for (int i = tid; i < slots; i += kRunThreads) {
+  for (int i = tid; i < slots; i += run_threads<F, MULTI>()) {
     mbar_init(smem_u32(full + i), 1);
     mbar_init(smem_u32(empty + i), 1);
   }
   if (tid == 0) {
     for (int i = 0; i < kRunItemSlots; ++i) {
       mbar_init(smem_u32(ifull + i), 1);
-      mbar_init(smem_u32(iempty + i), W);
+      mbar_init(smem_u32(iempty + i), W + (JOINER ? 1 : 0));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(cfull + i), W);
@@ -226,6 +238,78 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
   await_previous_kernel();
 
   // =================================================================== producers
+  // ---- the sum of the warps' parts of an item
+  // lane W * r + w makes the factor of warp w's part of row r, and leaves it where the part's
+  // maximum was.  No shuffles: beside waiting and computing warps one takes some 280 cycles
+  // here, and the four a row were what held the items up (64 sequences of 4 drafts over the
+  // 8-bit cache).  (Short code: this warp shares the instruction cache with
+  // the consumers' loop; unrolled by 4, 11 us more for 64 sequences of 4 drafts.)
+  auto join = [&](const RunItem& it, int cb) {
+    static_assert(W * HP == 32, "a lane per row and warp");
+    constexpr int LR = D / 4;  // lanes per row
+    const float* co = comb_o(cb);
+    float* cm = comb_m(cb);
+    const int rows = it.tn * it.heads, d = 4 * (lane % LR), row = lane / W;
+    float m[W], M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      m[w] = cm[w * HP + row];
+      M = fmaxf(M, m[w]);
+    }
+    const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < W; ++w) l = fmaf(ex2((m[w] - base) * kLog2e), cm[(W + w) * HP + row], l);
+    __syncwarp();
+    float f = ex2((cm[lane % W * HP + row] - base) * kLog2e);
+    const bool mine = lane % W == 0 && row < rows;
+    if (it.part < 0) {
+      f *= l == 0.f ? 0.f : __fdividef(1.f, l);  // every score -inf: an empty row
+      if (mine && p.lse_out) p.lse_out[row_of(it, row)] = M + logf(l);
+    } else if (mine) {
+      p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + row] = make_float2(M, l);
+    }
+    cm[lane % W * HP + row] = f;
+    __syncwarp();
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 32 / LR) {
+      const int r = r0 + lane / LR;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float fw = cm[w * HP + min(r, rows - 1)];
+        const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + min(r, rows - 1)) * OP + d);
+        a.x = fmaf(fw, v.x, a.x);
+        a.y = fmaf(fw, v.y, a.y);
+        a.z = fmaf(fw, v.z, a.z);
+        a.w = fmaf(fw, v.w, a.w);
+      }
+      if (r >= rows) continue;
+      if (it.part < 0)
+        *reinterpret_cast<uint2*>(p.out + row_of(it, r) * D + d) =
+            make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+      else
+        *reinterpret_cast<float4*>(p.part_o + (((size_t)blockIdx.x * 2 + it.part) * NR + r) * D + d) = a;
+    }
+  };
+  if (JOINER && warp == W + 2) {  // adds the parts of every item up
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      const int is = k % kRunItemSlots, cb = k & 1;
+      ok = waitw(smem_u32(ifull + is), (k / kRunItemSlots) & 1, abort_flag);
+      if (!ok) break;
+      const RunItem it = *item_rec(is);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(iempty + is));
+      if (it.ntile == 0) break;
+      ok = waitw(smem_u32(cfull + cb), (k >> 1) & 1, abort_flag);
+      if (!ok) break;
+      join(it, cb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
+    }
+    if (!ok && lane == 0) report(p.dev_err, INKLING_DEVERR_TIMEOUT);
+    return;
+  }
   // Both walk the run: warp W sends the tiles, warp W + 1 prepares the items.
   if (warp >= W) {
     const bool copier = warp == W;
@@ -333,59 +417,6 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
 #pragma unroll
       for (int i = 0; i < 3; ++i) dst[32 * i] = src[i];
     };
-    // ---- the sum of the warps' parts of an item
-    // lane W * r + w makes the factor of warp w's part of row r, and leaves it where the part's
-    // maximum was.  No shuffles: beside waiting and computing warps one takes some 280 cycles
-    // here, and the four a row were what held the items up (64 sequences of 4 drafts over the
-    // 8-bit cache).  (Short code: this warp shares the instruction cache with
-    // the consumers' loop; unrolled by 4, 11 us more for 64 sequences of 4 drafts.)
-    auto join = [&](const RunItem& it, int cb) {
-      static_assert(W * HP == 32, "a lane per row and warp");
-      constexpr int LR = D / 4;  // lanes per row
-      const float* co = comb_o(cb);
-      float* cm = comb_m(cb);
-      const int rows = it.tn * it.heads, d = 4 * (lane % LR), row = lane / W;
-      float m[W], M = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        m[w] = cm[w * HP + row];
-        M = fmaxf(M, m[w]);
-      }
-      const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < W; ++w) l = fmaf(ex2((m[w] - base) * kLog2e), cm[(W + w) * HP + row], l);
-      __syncwarp();
-      float f = ex2((cm[lane % W * HP + row] - base) * kLog2e);
-      const bool mine = lane % W == 0 && row < rows;
-      if (it.part < 0) {
-        f *= l == 0.f ? 0.f : __fdividef(1.f, l);  // every score -inf: an empty row
-        if (mine && p.lse_out) p.lse_out[row_of(it, row)] = M + logf(l);
-      } else if (mine) {
-        p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + row] = make_float2(M, l);
-      }
-      cm[lane % W * HP + row] = f;
-      __syncwarp();
-#pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += 32 / LR) {
-        const int r = r0 + lane / LR;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float fw = cm[w * HP + min(r, rows - 1)];
-          const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + min(r, rows - 1)) * OP + d);
-          a.x = fmaf(fw, v.x, a.x);
-          a.y = fmaf(fw, v.y, a.y);
-          a.z = fmaf(fw, v.z, a.z);
-          a.w = fmaf(fw, v.w, a.w);
-        }
-        if (r >= rows) continue;
-        if (it.part < 0)
-          *reinterpret_cast<uint2*>(p.out + row_of(it, r) * D + d) =
-              make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
-        else
-          *reinterpret_cast<float4*>(p.part_o + (((size_t)blockIdx.x * 2 + it.part) * NR + r) * D + d) = a;
-      }
-    };
     auto join_item = [&](int k) -> bool {
       const int cb = k & 1;
       if (!waitw(smem_u32(cfull + cb), (k >> 1) & 1, abort_flag)) return false;
@@ -437,7 +468,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
         if (dhi > dlo) bulk_prefetch_l2(row + dlo, (uint32_t)(dhi - dlo) * 4);
       }
       // (the record of item ki - 2 is in the slot of the item after this one)
-      if (!copier) ok = publish(it) && (ki < 3 || join_item(ki - 3));
+      if (!copier) ok = publish(it) && (JOINER || ki < 3 || join_item(ki - 3));
       if (!ok) break;
       // ---- its tiles: a lane each, a batch of at most 32 (and of the ring's slots: no
       // two lanes share one) at a time.  A lane's copies go out as soon as its slot is
@@ -543,7 +574,7 @@ __global__ void __launch_bounds__(kRunThreads, kRunCtas)
         RunItem end;
         memset(&end, 0, sizeof(end));
         const int n = ki;
-        ok = publish(end) && (n < 2 || join_item(n - 2)) && (n < 1 || join_item(n - 1));  // ntile = 0: no more items
+        ok = publish(end) && (JOINER || ((n < 2 || join_item(n - 2)) && (n < 1 || join_item(n - 1))));  // ntile = 0: no more items
       }
       if (lane == 0) p.cut[blockIdx.x] = cut;
       if (!ok && lane == 0) report(p.dev_err, INKLING_DEVERR_TIMEOUT);

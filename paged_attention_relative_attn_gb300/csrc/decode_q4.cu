@@ -60,6 +60,7 @@ __device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32
 }
 
 struct Q4Format {
+  static constexpr bool kJoiner = false;
   static constexpr int kGroup = 4;
   __host__ __device__ static constexpr int block_bytes(int D) { return q4_block_bytes(D); }
   // Rows 2t, 2t + 1 are keys t, 4 + (t ^ 1), so that the 64-byte rows read together lie in both halves
@@ -332,7 +333,7 @@ struct Q4Launch {
     auto kern = decode_blocks_kernel<Q4Format, D, MULTI>;
     static std::atomic<int> limit_set[kMaxDevices];
     return smem_limit_on_device(reinterpret_cast<const void*>(kern), kRunSmemBudget, limit_set) &&
-           launch_dependent(kern, dim3(plan.grid), kRunThreads, smem, p, c.stream) &&
+           launch_dependent(kern, dim3(plan.grid), run_threads<Q4Format, MULTI>(), smem, p, c.stream) &&
            launch_dependent(merge_blocks_kernel<D>, dim3(plan.grid, plan.NR), 32 * kRunMergeWarps, 0, p, c.stream);
   }
 };

@@ -42,6 +42,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 struct Q8Format {
+  static constexpr bool kJoiner = true;
   static constexpr int kGroup = 1;  // a ring of 8 tiles (32 sequences to 32768 keys: 190.2 us; in fours 193.8)
   __host__ __device__ static constexpr int block_bytes(int D) { return q8_block_bytes(D); }
   __device__ static int key_of(int g) { return g; }
@@ -275,7 +276,7 @@ struct Q8Launch {
     auto kern = decode_blocks_kernel<Q8Format, D, MULTI>;
     static std::atomic<int> limit_set[kMaxDevices];
     return smem_limit_on_device(reinterpret_cast<const void*>(kern), kRunSmemBudget, limit_set) &&
-           launch_dependent(kern, dim3(plan.grid), kRunThreads, smem, p, c.stream) &&
+           launch_dependent(kern, dim3(plan.grid), run_threads<Q8Format, MULTI>(), smem, p, c.stream) &&
            launch_dependent(merge_blocks_kernel<D>, dim3(plan.grid, plan.NR), 32 * kRunMergeWarps, 0, p, c.stream);
   }
 };
