@@ -681,7 +681,7 @@ int inkling_rel_attn_compact_pages(
  * i < n (and i < *count, where that is given).  Negative ids: skipped; ids past the
  * pool: INKLING_DEVERR_BAD_PAGE, skipped.  The dst pages of a call are distinct and
  * none of them is a src page of another pair.  (Skipped pairs are looked at for every
- * 64 KB that they would copy: a long list with few pairs at its head wants a count.)
+ * 32 KB that they would copy: a long list with few pairs at its head wants a count.)
  *
  *   pools       HOST array of n_pools device pointers, each 16-byte aligned, to
  *               num_pages pages of page_bytes bytes (a multiple of 16): K and V of
