@@ -660,7 +660,9 @@ int inkling_rel_attn_release_pages(
  * renumbered, the stack is rewritten with the lowest page on top; the pages' content
  * is moved by inkling_rel_attn_copy_pages with the list that the call makes, before
  * anything is appended.  Pages that are neither live nor on the stack are left alone.  A
- * live page that is on the stack too: INKLING_DEVERR_BAD_PAGE, it stays in use.
+ * live page that is on the stack too, or a page that is on it twice:
+ * INKLING_DEVERR_BAD_PAGE; the live one stays in use, the other stays on the stack once, and
+ * the stack keeps its height, with -1 at its bottom.
  *
  *   seq_lens      int32 [B], tokens held
  *   page_table    int32 [B, page_table_stride], updated in place

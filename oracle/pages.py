@@ -75,7 +75,7 @@ def ref_compact(seq_lens, table, refs, free, count, P):
     n = len(free)
     live = sorted({int(table[b, c]) for b in range(len(seq_lens)) for c in range(pages_for(seq_lens[b], P))})
     stack = {int(x) for x in free[:count]}
-    bits = {"bad_page"} if stack & set(live) else set()
+    bits = {"bad_page"} if stack & set(live) or len(stack) < count else set()
     known = sorted(set(live) | stack)
     low, high = known[:len(live)], known[len(live):]
     src = [x for x in high if x in live]
@@ -86,7 +86,7 @@ def ref_compact(seq_lens, table, refs, free, count, P):
             table[b, c] = to.get(int(table[b, c]), table[b, c])
     for a, z in to.items():
         refs[z], refs[a] = refs[a], 0
-    free[:len(high)] = high[::-1]
+    free[:count] = [-1] * (count - len(high)) + high[::-1]
     pad = [-1] * (n - len(src))
     return dict(table=table, refs=refs, free=free, src=np.array(src + pad), dst=np.array(dst + pad), moves=len(src),
                 bits=bits)

@@ -288,8 +288,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
   }
   for (int i = tid; i < F; i += kPgThreads) {
     const int page = p.free_pages[i];
-    if (page_ok(p, page)) atomicOr(spare + page / 32, 1u << page % 32);
-    else report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+    const uint32_t bit = 1u << page % 32;
+    if (!page_ok(p, page) || (atomicOr(spare + page / 32, bit) & bit)) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
   }
   __syncthreads();
   // a thread's words; pages of either kind before them
@@ -329,6 +329,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
   int both;
   int at = scan_block(moving, scratch, both);
   const int moves = both / 2;  // as many holes as moving pages; the holes come first
+  // places of the stack without a page (it held one twice, a live one or none): at the bottom, and no page's id,
+  // so that build_tables tells whoever gets one and never hands out a live page
+  for (int i = tid; i < F - (all_known - all_live); i += kPgThreads) p.free_pages[i] = -1;
   int r = known0;
   for (int w = w0; w < w1; ++w) {
     before[w] = (uint32_t)at;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
     // the stack: the pages from the border on, the lowest on top
     const uint32_t k = live[w] | spare[w];
     for (uint32_t m = k; m != 0u; m &= m - 1, ++r)
-      if (r >= all_live) p.free_pages[all_known - 1 - r] = 32 * w + __ffs(m) - 1;
+      if (r >= all_live) p.free_pages[F - 1 - (r - all_live)] = 32 * w + __ffs(m) - 1;
   }
   for (int i = moves + tid; i < p.num_pages; i += kPgThreads) p.src[i] = p.dst[i] = -1;
   if (tid == 0) *p.count = moves;

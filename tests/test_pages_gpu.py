@@ -193,6 +193,22 @@ def test_compact_edges(ops):
     assert int(err) == 1 and int(moves) == want["moves"] and np.array_equal(d["table"].cpu().numpy(), want["table"])
 
 
+@pytest.mark.parametrize("lens,spoil", [([40, 33], "live"), ([40, 33], "twice"), ([16] * 70, "both")])
+def test_compact_of_a_spoiled_stack(ops, lens, spoil):
+    """A live page on the stack, a page on it twice: what is taken off the stack afterwards is no live page."""
+    s = State(lens, 16, 4, 9, 21)
+    if spoil in ("live", "both"):
+        s.free[7] = s.table[0, 0]
+    if spoil in ("twice", "both"):
+        s.free[2] = s.free[5]
+    want = check_compact(ops, s, refs=False)
+    assert want["bits"] == {"bad_page"}
+    live = {int(s.table[b, c]) for b, L in enumerate(lens) for c in range(pages_for(L, 16))}
+    got = [int(x) for x in s.free[:s.count]]
+    kept = [x for x in got if x >= 0]
+    assert not live & set(kept) and len(set(kept)) == len(kept) and got[:len(got) - len(kept)] == [-1] * (len(got) - len(kept))
+
+
 def test_compact_without_rows(ops):
     e = torch.empty(0, dtype=torch.int32, device=DEV)
     free = i32([5, 1, 3, 0, 0, 0])
