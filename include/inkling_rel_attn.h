@@ -635,12 +635,12 @@ int inkling_rel_attn_fork_pages(
  * inkling_rel_attn_release_pages -- pages of ended requests (new_lens[b] < 0).  Every
  * page of such a row loses an owner; one without owners goes on the stack: in batch
  * order and each row in page order, a page that several of the rows owned at the last
- * of them.  More rows than page_refs knows owners: INKLING_DEVERR_BAD_PAGE, the page
- * goes back once.  A stack that would grow past num_pages:
+ * of them.  More entries than page_refs knows owners (in several rows or in one):
+ * INKLING_DEVERR_BAD_PAGE, the page goes back once, in the place of the last entry.  A stack that would grow past num_pages:
  * INKLING_DEVERR_BAD_PAGE, the pages past it are dropped.
  *
  *   seq_lens      int32 [B], tokens held; new_lens int32 [B], as for build_tables
- *   page_table    int32 [B, page_table_stride], read
+ *   page_table    int32 [B, page_table_stride], read; B * page_table_stride up to 2^30
  *   page_refs     int32 [num_pages], updated in place
  *   free_pages    int32 [num_pages], returned pages written above the top; free_count int32 [1]
  *   kv_lens       int32 [B], out: seq_lens, but 0 for the ended.  May be seq_lens itself

@@ -63,6 +63,7 @@ int inkling_rel_attn_release_pages(const int32_t* seq_lens, const int32_t* new_l
                                    int32_t* kv_lens, int32_t* free_left, int32_t* device_error, void* stream) {
   const int rc = tables_shape(page_table_stride, B, page_size, num_pages);
   if (rc != INKLING_OK) return rc;
+  if ((int64_t)B * page_table_stride > kReleaseMaxEntries) return INKLING_ERR_ARG;
   if (B == 0) return INKLING_OK;
   if (!seq_lens || !new_lens || !page_table || !page_refs || !free_pages || !free_count || !kv_lens || !free_left)
     return INKLING_ERR_ARG;

@@ -197,6 +197,7 @@ struct PagesCall {
   cudaStream_t stream;
 };
 
+constexpr int64_t kReleaseMaxEntries = 1 << 30;  // B * page_table_stride of a release: the marks in page_refs
 constexpr int32_t kCompactMaxPages = 1 << 19;  // of a pool that is compacted: 12 bytes of shared memory for 32
 
 struct CopyPagesCall {

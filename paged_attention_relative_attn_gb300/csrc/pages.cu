@@ -162,10 +162,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) fork_pages_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 // Release.  Four steps over the entries of the ended rows: the owners of each page are
-// counted down; of a page without owners the last of the rows (the highest) is found by a
-// minimum over -kMark - row in its counter; each row counts the pages that it gives
-// back; they go to their places on the stack and their counters to 0.
-constexpr int kMark = 1 << 20;  // past every count of rows
+// counted down; of a page without owners the last entry (the highest, one alone even if a row holds
+// the page twice) is found by a minimum over marks in its counter; each row counts the pages
+// that it gives back; they go to their places on the stack and their counters to 0.
+constexpr int kMark = 1 << 30;  // past every count of entries, at most kReleaseMaxEntries
+__device__ __forceinline__ int mark_of(const PagesParams& p, int b, int c) { return -kMark - (b * p.pt_stride + c); }
 
 __device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t block) {
   uint32_t r;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) release_pages_kernel(const __gr
     for (int c = lane; c < n; c += 32) {
       const int page = p.page_table[(size_t)b * p.pt_stride + c];
       if (!page_ok(p, page) || __ldcg(p.page_refs + page) >= 0) continue;
-      const int was = atomicMin(p.page_refs + page, -kMark - b);
+      const int was = atomicMin(p.page_refs + page, mark_of(p, b, c));
       if (was > -kMark && was < -1) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);  // more rows than owners
     }
   }
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) release_pages_kernel(const __gr
     int mine = 0;
     for (int c = lane; c < n; c += 32) {
       const int page = p.page_table[(size_t)b * p.pt_stride + c];
-      mine += page_ok(p, page) && __ldcg(p.page_refs + page) == -kMark - b ? 1 : 0;
+      mine += page_ok(p, page) && __ldcg(p.page_refs + page) == mark_of(p, b, c) ? 1 : 0;
     }
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane < (int)gridDim.x && n > 0)  // into every block's copy
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) release_pages_kernel(const __gr
     for (int c0 = 0; c0 < n; c0 += 32) {
       const int c = c0 + lane;
       const int page = c < n ? p.page_table[(size_t)b * p.pt_stride + c] : -1;
-      const bool mine = page_ok(p, page) && __ldcg(p.page_refs + page) == -kMark - b;
+      const bool mine = page_ok(p, page) && __ldcg(p.page_refs + page) == mark_of(p, b, c);
       const uint32_t who = __ballot_sync(0xffffffffu, mine);
       if (mine) {
         const int place = to + __popc(who & ((1u << lane) - 1u));

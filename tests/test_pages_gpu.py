@@ -167,6 +167,23 @@ def test_release_reports_what_cannot_be(ops):
 
 
 @pytest.mark.parametrize("seed", range(4))
+def test_release_of_a_page_twice_in_a_row(ops, seed):
+    """Entries next to each other, in the same 32 of a row, far apart, and in other rows: back once, no place left out."""
+    rng = np.random.default_rng(seed)
+    s = State([100 * 16, 40 * 16, 3 * 16, 17], 16, 101, 5, 30 + seed)
+    at = [(0, 0), (0, 1), (0, 40), (1, 39), (2, 2)]
+    page = s.table[0, 7]
+    for b, c in at[:2 + seed]:
+        s.table[b, c] = page
+    for _ in range(seed):
+        s.table[1, rng.integers(40)] = s.table[1, rng.integers(40)]
+    want = check_release(ops, s, [-1, -1, -1, 2])
+    assert want["bits"] == {"bad_page"} and not want["refs"].any()
+    stack = want["free"][:want["left"]]
+    assert len(set(stack.tolist())) == len(stack)
+
+
+@pytest.mark.parametrize("seed", range(4))
 def test_compact(ops, seed):
     rng = np.random.default_rng(seed)
     lens = list(rng.integers(0, 200, 7)) + [0] * 3

@@ -89,6 +89,17 @@ def test_calls_and_packed_calls_check_every_argument(lib, name):
     assert f(*[1 << 28 if s[0] == "stride" else g for s, g in zip(spec, good)]) == -1
 
 
+def test_release_table_size(lib):
+    f = lib.inkling_rel_attn_release_pages
+    assert f(4, 4, 4, (1 << 17) + 1, 4, 4, 4, 8192, 16, 8, 4, 4, 4, 0) == -1
+    assert f(4, 4, 4, 1 << 17, 4, 4, 2, 8192, 16, 8, 4, 4, 4, 0) == -2  # the size is taken, the address is not
+
+
+def test_row_that_holds_a_page_twice():
+    r = ref_release([48, 16], [-1, -1], np.array([[3, 3, 2], [1, 0, 0]]), np.zeros(4, dtype=int), np.zeros(4, dtype=int), 0, 16)
+    assert list(r["free"]) == [3, 2, 1, 0] and r["left"] == 3 and r["bits"] == {"bad_page"} and not r["refs"].any()
+
+
 def test_compact_pool_size(lib):
     spec = plain_args()["compact_pages"]
     args = [(1 << 19) + 1 if s[0] == "num_pages" else s[1] for s in spec]
