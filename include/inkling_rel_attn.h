@@ -548,6 +548,9 @@ int inkling_rel_attn_kv_read_q8(
  * last q_len (1 .. 64) tokens of each sequence, on the values x * 2^e.  Keys past a
  * row's position or window, and places past a sequence's end, may hold any bytes;
  * the blocks that hold a visible key are as the append left them.
+ *   A row with a NaN that a token sees makes its outputs NaN, in K (out and lse) and in V
+ * (out), whatever the key's bias (-inf too) and weight (0 too); but where all scores are
+ * -inf, out = 0 whatever V holds.  Tokens that do not see it keep their bits.
  *   Range: q to 2^60, |scale| <= 2^54 (checked), |scale| times the largest |q| and |k|
  * to 2^100 (q of a row and K of a block enter as numbers relative to their largest
  * magnitude: what a q value loses lies below 2^-39 of its row's largest).  V blocks

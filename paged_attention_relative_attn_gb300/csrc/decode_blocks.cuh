@@ -36,7 +36,8 @@
 //   prepare          q of an item's rows as operands, and up to 4 words beside (RunPrep::extra)
 //   kGroup           tiles whose copies go out together (those of a long ring)
 //   kJoiner          whether a third producer warp fits the registers
-//   Consumer         the products S^T = K Q^T (16 keys x rows) and O^T += V^T P^T of a warp
+//   Consumer         the products S^T = K Q^T (16 keys x rows) and O^T += V^T P^T of a warp;
+//                    mark: what rows get from keys with a NaN that they see
 #pragma once
 
 #include <cuda_bf16.h>
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
     float f = ex2((cm[lane % W * HP + row] - base) * kLog2e);
     const bool mine = lane % W == 0 && row < rows;
     if (it.part < 0) {
-      f *= l == 0.f ? 0.f : __fdividef(1.f, l);  // every score -inf: an empty row
+      f = l == 0.f ? -1.f : f * __fdividef(1.f, l);  // every score -inf: an empty row, whatever its values
       if (mine && p.lse_out) p.lse_out[row_of(it, row)] = M + logf(l);
     } else if (mine) {
       p.part_ml[((size_t)blockIdx.x * 2 + it.part) * NR + row] = make_float2(M, l);
@@ -274,9 +275,11 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
     for (int r0 = 0; r0 < rows; r0 += 32 / LR) {
       const int r = r0 + lane / LR;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      bool empty = false;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float fw = cm[w * HP + min(r, rows - 1)];
+        if (w == 0) empty = fw < 0.f;
         const float4 v = *reinterpret_cast<const float4*>(co + (w * NR + min(r, rows - 1)) * OP + d);
         a.x = fmaf(fw, v.x, a.x);
         a.y = fmaf(fw, v.y, a.y);
@@ -284,6 +287,7 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
         a.w = fmaf(fw, v.w, a.w);
       }
       if (r >= rows) continue;
+      if (empty) a = make_float4(0.f, 0.f, 0.f, 0.f);
       if (it.part < 0)
         *reinterpret_cast<uint2*>(p.out + row_of(it, r) * D + d) =
             make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
@@ -732,6 +736,11 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
         l_run[0] += sc[u][0] + sc[u][2];
         l_run[1] += sc[u][1] + sc[u][3];
       }
+      // (whether the row of weight x sees its key: by position and window, whatever the bias)
+      c.mark(ring_slot, sc, l_run, [&](int u, int x) {
+        const int dist = pr.pos[x & 1] - key_g - (key0 + 16 * u + 8 * (x >> 1));
+        return dist >= 0 && (p.window <= 0 || dist < p.window);
+      });
       // ---- O^T += V^T P^T; hands the slot back
       c.values(ring_slot, eb, sc);
     }

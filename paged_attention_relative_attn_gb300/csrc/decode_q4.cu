@@ -252,6 +252,9 @@ struct Q4Format {
       const float s = fmaf(raw, p.scale, bias);
       return MULTI && hidden ? -INFINITY : s;  // (of a key that other rows see: its scale may be NaN)
     }
+    template <class Sees>
+    __device__ __forceinline__ void mark(const uint8_t*, float (&)[U][4], float (&)[2], const Sees&) const {
+    }  // a NaN is in its group's scale
     __device__ __forceinline__ bool v_scales(const uint8_t*) { return false; }  // V has no base
     __device__ __forceinline__ float v_rebase() { return 1.f; }
     __device__ __forceinline__ void rescale(int x, float al) {
