@@ -616,7 +616,9 @@ size_t inkling_rel_attn_prefill_q8_workspace_size(int32_t B, int32_t max_q_len,
  * top, in batch order; a row that needs one and finds none is refused
  * (INKLING_DEVERR_NO_PAGES): it stays empty.  A row that holds tokens already, or whose
  * source is not a row: INKLING_DEVERR_BAD_SLOT, left as it is.  A source longer than its
- * row: INKLING_DEVERR_SEQ_TOO_LONG, the fork stays empty.
+ * row: INKLING_DEVERR_SEQ_TOO_LONG, the fork stays empty.  A page id outside [0, num_pages) among
+ * those of a source's tokens: INKLING_DEVERR_BAD_PAGE, the fork stays empty and takes no page;
+ * one on the stack: the same, for the row that would get it, and the entry leaves the stack.
  *
  *   source        int32 [B]; -1: nothing to do
  *   seq_lens      int32 [B], tokens held

@@ -29,16 +29,22 @@ def ref_fork(source, seq_lens, table, refs, free, count, P):
             bits.add("too_long")
             continue
         full = n // P
+        if any(not 0 <= page < len(free) for page in table[s, :pages_for(n, P)]):
+            bits.add("bad_page")
+            continue
         if n % P and top == 0:
             bits.add("no_pages")
             continue
+        if n % P:
+            top -= 1
+            if not 0 <= free[top] < len(free):
+                bits.add("bad_page")
+                continue
+            src[b], dst[b] = table[s, full], free[top]
+            table[b, full] = free[top]
         for c in range(full):
             table[b, c] = table[s, c]
             refs[table[s, c]] += 1
-        if n % P:
-            top -= 1
-            src[b], dst[b] = table[s, full], free[top]
-            table[b, full] = free[top]
         kv[b] = n
     return dict(kv_lens=kv, table=table, refs=refs, src=src, dst=dst, left=top, bits=bits)
 

@@ -81,21 +81,38 @@ __device__ __forceinline__ int scan_block(int x, int* scratch, int& total) {
 }
 
 // ---------------------------------------------------------------------------
-// Fork.  Every block of the cluster makes the ranks of the requests that need a page; rows
-// are then shared out over the cluster's warps.
+// Fork.  Rows are shared out over the cluster's warps, which look at the pages of each fork's
+// source first: a fork with one that is none becomes a fork of no tokens.  Then every block makes the
+// ranks of the requests that need a page, and the rows are written.
+__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t block) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(block));
+  return r;
+}
+// Every block's copy of a word of shared memory; a warp calls it.
+__device__ __forceinline__ void set_in_cluster(const int32_t* word, int value) {
+  const uint32_t block = threadIdx.x & 31;
+  if (block < gridDim.x)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(word, block)), "r"(value) : "memory");
+}
+
 __global__ void __launch_bounds__(kPgThreads, 1) fork_pages_kernel(const __grid_constant__ PagesParams p) {
-  await_previous_kernel();
   extern __shared__ int32_t sm[];
-  int32_t* rank_of = sm;        // [B] rank of the page it takes; -1: none needed; -2: not served
-  int32_t* lens = sm + p.B;     // [B] tokens it gets; -1: no fork
+  int32_t* refused = sm;             // [B] not 0: its source has a page that is none
+  int32_t* lens = refused + p.B;     // [B] tokens it gets; -1: no fork
+  int32_t* source = lens + p.B;      // [B]
+  int32_t* page_for = source + p.B;  // [B] the page that it takes; -1: none needed; -2: not served
   __shared__ int scratch[kPgWarps + 1];
   __shared__ int s_used;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int w0 = (int)blockIdx.x * kPgWarps + warp, dw = (int)gridDim.x * kPgWarps;
   const bool first = blockIdx.x == 0;
+  for (int b = tid; b < p.B; b += kPgThreads) refused[b] = 0;
+  if (tid == 0) s_used = 0;
+  cluster_arrive();  // waited for where another block's copy is written
+  await_previous_kernel();
   const int F = min(max(*p.free_count, 0), p.num_pages), cap = p.pt_stride * p.P;
   const int per = (p.B + kPgThreads - 1) / kPgThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  if (tid == 0) s_used = 0;
-  int need = 0;
   for (int b = b0; b < b1; ++b) {
     const int from = p.source[b];
     int n = -1;
@@ -108,55 +125,76 @@ __global__ void __launch_bounds__(kPgThreads, 1) fork_pages_kernel(const __grid_
       if (!bad && !long_) n = max(L, 0);
     }
     lens[b] = n;
-    const bool part = n > 0 && n % p.P != 0;
-    rank_of[b] = part ? 0 : -1;
-    need += part ? 1 : 0;
+    source[b] = from;
+  }
+  cluster_wait();
+  __syncthreads();
+  for (int b = w0; b < p.B; b += dw) {
+    const int n = lens[b];
+    if (n <= 0) continue;
+    const int32_t* parent = p.page_table + (size_t)source[b] * p.pt_stride;
+    bool none = false;
+    const int held = pages_of(p, n);
+#pragma unroll 4
+    for (int c = lane; c < held; c += 32) none |= !page_ok(p, parent[c]);
+    if (!__any_sync(0xffffffffu, none)) continue;
+    if (lane == 0) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+    set_in_cluster(refused + b, 1);
+  }
+  cluster_arrive();  // this block has read the lengths that kv_lens may replace, and the stack's height
+  cluster_wait();
+  int need = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (refused[b]) lens[b] = 0;
+    need += lens[b] > 0 && lens[b] % p.P != 0 ? 1 : 0;
   }
   int all;
   int at = scan_block(need, scratch, all);
   int used = 0;
   for (int b = b0; b < b1; ++b) {
-    if (rank_of[b] < 0) continue;
-    const bool served = at < F;
-    rank_of[b] = served ? at : -2;
-    if (served) used = at + 1;
-    else if (first) report(p.dev_err, INKLING_DEVERR_NO_PAGES);
+    page_for[b] = -1;
+    if (lens[b] <= 0 || lens[b] % p.P == 0) continue;
+    int page = -2;
+    if (at < F) {
+      used = at + 1;
+      page = p.free_pages[F - 1 - at];
+      if (!page_ok(p, page)) {  // it leaves the stack all the same
+        if (first) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+        page = -2;
+      }
+    } else if (first) {
+      report(p.dev_err, INKLING_DEVERR_NO_PAGES);
+    }
+    page_for[b] = page;
     ++at;
   }
   if (used > 0) atomicMax(&s_used, used);
   __syncthreads();
-  cluster_arrive();  // this block has read the lengths and the stack's height
-  for (int b = (int)blockIdx.x * kPgWarps + warp; b < p.B; b += (int)gridDim.x * kPgWarps) {
-    const int n = lens[b], rank = rank_of[b];
-    int src = -1, dst = -1;
-    if (n > 0 && rank != -2) {
-      const int32_t* parent = p.page_table + (size_t)p.source[b] * p.pt_stride;
+  for (int b = w0; b < p.B; b += dw) {
+    const int n = lens[b], dst = page_for[b];
+    int src = -1;
+    if (n > 0 && dst != -2) {
+      const int32_t* parent = p.page_table + (size_t)source[b] * p.pt_stride;
       int32_t* row = p.page_table + (size_t)b * p.pt_stride;
       const int full = pages_of(p, n - p.P + 1);  // n / P (n - P + 1 + P - 1 = n)
       for (int c = lane; c < full; c += 32) {
         const int page = parent[c];
         row[c] = page;
-        if (page_ok(p, page)) atomicAdd(p.page_refs + page, 1);
-        else report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+        atomicAdd(p.page_refs + page, 1);
       }
-      if (rank >= 0) {
+      if (dst >= 0) {
         src = parent[full];
-        dst = p.free_pages[F - 1 - rank];
-        if (lane == 0) {
-          row[full] = dst;
-          if (!page_ok(p, src) || !page_ok(p, dst)) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
-        }
+        if (lane == 0) row[full] = dst;
       }
     }
     if (lane == 0) {
       p.src[b] = src;
-      p.dst[b] = dst;
+      p.dst[b] = src < 0 ? -1 : dst;
     }
   }
-  cluster_wait();  // kv_lens may be seq_lens, the height free_count: every block has read them
   if (!first) return;
   for (int b = tid; b < p.B; b += kPgThreads)
-    p.kv_lens[b] = lens[b] < 0 ? p.seq_lens[b] : rank_of[b] == -2 ? 0 : lens[b];
+    p.kv_lens[b] = lens[b] < 0 ? p.seq_lens[b] : page_for[b] == -2 ? 0 : lens[b];
   if (tid == 0) *p.count = F - s_used;
 }
 
@@ -167,12 +205,6 @@ __global__ void __launch_bounds__(kPgThreads, 1) fork_pages_kernel(const __grid_
 // that it gives back; they go to their places on the stack and their counters to 0.
 constexpr int kMark = 1 << 30;  // past every count of entries, at most kReleaseMaxEntries
 __device__ __forceinline__ int mark_of(const PagesParams& p, int b, int c) { return -kMark - (b * p.pt_stride + c); }
-
-__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t block) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(block));
-  return r;
-}
 
 __global__ void __launch_bounds__(kPgThreads, 1) release_pages_kernel(const __grid_constant__ PagesParams p) {
   await_previous_kernel();
@@ -216,8 +248,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) release_pages_kernel(const __gr
       mine += page_ok(p, page) && __ldcg(p.page_refs + page) == mark_of(p, b, c) ? 1 : 0;
     }
     mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane < (int)gridDim.x && n > 0)  // into every block's copy
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(back + b, lane)), "r"(mine) : "memory");
+    if (n > 0) set_in_cluster(back + b, mine);
   }
   cluster_arrive();
   cluster_wait();
@@ -461,10 +492,10 @@ static unsigned row_blocks(int B) { return (unsigned)std::min(8, (B + kPgWarps -
 
 int launch_fork_pages(const PagesCall& c) {
   static std::atomic<int> limit_set[kMaxDevices];
-  if (!smem_limit_on_device(reinterpret_cast<const void*>(fork_pages_kernel), 8 * kTablesMaxBatch, limit_set))
+  if (!smem_limit_on_device(reinterpret_cast<const void*>(fork_pages_kernel), 16 * kTablesMaxBatch, limit_set))
     return INKLING_ERR_CUDA;
   const unsigned blocks = row_blocks(c.B);
-  return launch_dependent(fork_pages_kernel, dim3(blocks), kPgThreads, 8 * c.B, pages_params(c), c.stream, blocks)
+  return launch_dependent(fork_pages_kernel, dim3(blocks), kPgThreads, 16 * c.B, pages_params(c), c.stream, blocks)
              ? INKLING_OK
              : INKLING_ERR_CUDA;
 }
