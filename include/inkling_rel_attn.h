@@ -667,7 +667,8 @@ int inkling_rel_attn_release_pages(
  * anything is appended.  Pages that are neither live nor on the stack are left alone.  A
  * live page that is on the stack too, or a page that is on it twice:
  * INKLING_DEVERR_BAD_PAGE; the live one stays in use, the other stays on the stack once, and
- * the stack keeps its height, with -1 at its bottom.
+ * the stack keeps its height, with -1 at its bottom (as for an id that is none).  Places with
+ * -1 are not told again by a later call; who is to get such a page is (build_tables, fork_pages).
  *
  *   seq_lens      int32 [B], tokens held
  *   page_table    int32 [B, page_table_stride], updated in place

@@ -80,8 +80,9 @@ def ref_compact(seq_lens, table, refs, free, count, P):
     table, refs, free = table.copy(), refs.copy(), free.copy()
     n = len(free)
     live = sorted({int(table[b, c]) for b in range(len(seq_lens)) for c in range(pages_for(seq_lens[b], P))})
-    stack = {int(x) for x in free[:count]}
-    bits = {"bad_page"} if stack & set(live) or len(stack) < count else set()
+    named = [int(x) for x in free[:count] if x != -1]  # (-1: a place without a page, as a compaction leaves it)
+    stack = {x for x in named if 0 <= x < n}
+    bits = {"bad_page"} if stack & set(live) or len(stack) < len(named) else set()
     known = sorted(set(live) | stack)
     low, high = known[:len(live)], known[len(live):]
     src = [x for x in high if x in live]

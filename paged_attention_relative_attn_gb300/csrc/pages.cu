@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
   }
   for (int i = tid; i < F; i += kPgThreads) {
     const int page = p.free_pages[i];
-    const uint32_t bit = 1u << page % 32;
-    if (!page_ok(p, page) || (atomicOr(spare + page / 32, bit) & bit)) report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
+    if (page == -1) continue;  // a place without a page, which an earlier compaction has told of
+    if (!page_ok(p, page) || (atomicOr(spare + page / 32, 1u << page % 32) >> page % 32 & 1u))
+      report(p.dev_err, INKLING_DEVERR_BAD_PAGE);
   }
   __syncthreads();
   // a thread's words; pages of either kind before them
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) compact_pages_kernel(const __gr
   int at = scan_block(moving, scratch, both);
   const int moves = both / 2;  // as many holes as moving pages; the holes come first
   // places of the stack without a page (it held one twice, a live one or none): at the bottom, and no page's id,
-  // so that build_tables tells whoever gets one and never hands out a live page
+  // so that build_tables and fork_pages tell whoever gets one and never hand out a live page
   for (int i = tid; i < F - (all_known - all_live); i += kPgThreads) p.free_pages[i] = -1;
   int r = known0;
   for (int w = w0; w < w1; ++w) {
