@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
         __syncwarp();
       }
       if (valid && grp == 0 && p.lse_out)
-        p.lse_out[(size_t)(t0 + i) * p.H_q + h] = L > 0.f ? M + log2f(L) * kLn2 : -INFINITY;
+        p.lse_out[(size_t)(t0 + i) * p.H_q + h] = L == 0.f ? -INFINITY : M + log2f(L) * kLn2;  // (a NaN stays one)
     } else if (lane == 0) {
       report(p.dev_err, INKLING_DEVERR_TIMEOUT);
     }
