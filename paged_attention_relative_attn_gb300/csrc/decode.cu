@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm)
         Ls = fmaf(sc[w], comb_l[w * HP + h], Ls);
       }
       float lse;
-      if constexpr (MULTI) lse = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+      if constexpr (MULTI) lse = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
       else lse = (M + log2f(Ls)) * kLn2;
       const size_t row = out_row(h);
       if (final_out) {
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm)
       }
 #pragma unroll
       for (int w = 0; w < kCombSlots; ++w) comb_m[w * HP + h] = sc[w];
-      if constexpr (MULTI) comb_l[h] = Ls > 0.f ? 1.f / Ls : 0.f;
+      if constexpr (MULTI) comb_l[h] = Ls == 0.f ? 0.f : 1.f / Ls;
       else comb_l[h] = 1.f / Ls;
       reinterpret_cast<int*>(comb_l)[HP + h] = (int)row;
     }
@@ -1081,17 +1081,18 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
   for (int s = lane; s < n; s += 32) M = fmaxf(M, lse[s]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
   float z = 0.f;
-  for (int s = lane; s < n; s += 32) z += ex2((lse[s] - M) * kLog2e);
+  for (int s = lane; s < n; s += 32) z += ex2((lse[s] - base) * kLog2e);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-  const float LSE = M > -INFINITY ? M + logf(z) : -INFINITY;
+  const float LSE = base + logf(z);  // -inf where every split is empty (z = 0), NaN where one is
   constexpr int PER = D / 32;
   float acc[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) acc[j] = 0.f;
   const float* o = p.o_part + (size_t)idx * p.S * D + lane * PER;
-  for (int s = 0; s < n && LSE > -INFINITY; ++s) {
+  for (int s = 0; s < n && LSE != -INFINITY; ++s) {
     const float w = ex2((lse[s] - LSE) * kLog2e);
     if constexpr (PER == 4) {
       const float4 v = *reinterpret_cast<const float4*>(o + (size_t)s * D);
