@@ -432,7 +432,9 @@ int inkling_rel_attn_kv_read_q4(
  * cache: the last q_len (1 .. 64) tokens of each sequence, q_len = 1 being plain
  * decode.  Same formula on the values x * s, same shapes, lengths and errors;
  * one more rule: a row all of whose visible scores are -inf gets out = 0, lse =
- * -inf.  Keys past a row's position or window, and places past a sequence's
+ * -inf.  A NaN in a row of the cache that a token sees makes its outputs NaN, in K out and lse, in V the
+ * channels of out that have it, whatever the key's bias (-inf too) and weight (0 too; but for the
+ * rule before).  Keys past a row's position or window, and places past a sequence's
  * end, may hold any bytes; page ids of pages wholly before every row's window are
  * not looked at.
  *   The work is cut over the GPU by the batch's lengths, read on the device:

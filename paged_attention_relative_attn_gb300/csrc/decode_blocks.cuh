@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
       // ---- bias, on its way while the tile is awaited and K multiplied
       const bool inside = key0 + TK - 1 <= pos0 && (p.window <= 0 || pos1 - key0 < p.window);
       float bv[U][4];
+      uint32_t hidden = 0;  // bit 4 u + x: the row of score x does not see its key, whatever the bias
       const bool far = inside && pos0 - (key0 + TK - 1) >= p.R - 1;
       if (!far && inside && pos1 - key0 < p.R) {
 #pragma unroll
@@ -663,7 +664,9 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
           for (int x = 0; x < 4; ++x) {
             const int key = key0 + 16 * u + 8 * (x >> 1), dist = pr.pos[x & 1] - key_g - key;
             const float v = load_bias(pr.bias[x & 1] - key + (min(max(dist, 0), p.R - 1) - dist));
-            bv[u][x] = dist >= 0 && (p.window <= 0 || dist < p.window) ? v : -INFINITY;
+            const bool seen = dist >= 0 && (p.window <= 0 || dist < p.window);
+            bv[u][x] = seen ? v : -INFINITY;
+            hidden |= seen ? 0u : 1u << (4 * u + x);
           }
       }
       if (!waitw(smem_u32(full + s_slot), s_phase, abort_flag)) {
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sc[u][x] = c.score(p, u, x, sc[u][x], bv[u][x], bv[u][x] == -INFINITY);
+          for (int x = 0; x < 4; ++x) sc[u][x] = c.score(p, u, x, sc[u][x], bv[u][x], hidden >> (4 * u + x) & 1u);
       }
       // ---- running maximum and sum.  The maximum, the exponents' base, is
       // taken anew over the warp only when a score passes it by kRunSlack;
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(run_threads<F, MULTI>(), kRunCtas)
         return dist >= 0 && (p.window <= 0 || dist < p.window);
       });
       // ---- O^T += V^T P^T; hands the slot back
-      c.values(ring_slot, eb, sc);
+      c.values(ring_slot, eb, sc, hidden);
     }
     if (!ok) break;
 

@@ -268,7 +268,8 @@ struct Q4Format {
         }
       }
     }
-    __device__ __forceinline__ void values(const uint8_t* slot, uint32_t slot_bar, const float (&sc)[U][4]) {
+    __device__ __forceinline__ void values(const uint8_t* slot, uint32_t slot_bar, const float (&sc)[U][4],
+                                           uint32_t hidden) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint8_t* vp = slot + (U + u) * BLK;
@@ -300,7 +301,7 @@ struct Q4Format {
           float w[4] = {sc[u][0] * s0, sc[u][1] * s0, sc[u][2] * s8, sc[u][3] * s8};
           if constexpr (MULTI) {  // a key hidden from some of the rows: its scale may be NaN
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = sc[u][x] == 0.f ? 0.f : w[x];
+            for (int x = 0; x < 4; ++x) w[x] = hidden >> (4 * u + x) & 1u ? 0.f : w[x];
           }
           pb[0] = movmatrix_t(pack_bf16(w[0], w[1]));
           pb[1] = movmatrix_t(pack_bf16(w[2], w[3]));

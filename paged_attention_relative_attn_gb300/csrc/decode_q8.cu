@@ -235,7 +235,7 @@ struct Q8Format {
         o[j][x + 2] *= al;
       }
     }
-    __device__ __forceinline__ void values(const uint8_t* slot, uint32_t slot_bar, const float (&sc)[U][4]) {
+    __device__ __forceinline__ void values(const uint8_t* slot, uint32_t slot_bar, const float (&sc)[U][4], uint32_t) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint8_t* vp = slot + (U + u) * BLK;
