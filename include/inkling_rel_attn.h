@@ -368,7 +368,7 @@ int inkling_rel_attn_build_tables(
  * it: a sequence with fewer tokens than its rows is skipped by kv_append,
  * kv_conv_append (its convolution state too), prefill and prefill_q4
  * (INKLING_DEVERR_BAD_CHUNK), and gets out = 0, lse = -inf from the decode calls.
- * A staging pool for the convolution ahead of kv_append_q4 has lengths of its own: the
+ * A staging pool for the convolution ahead of kv_append_q4 or kv_append_q8 has lengths of its own: the
  * step's new tokens where step_lens > 0, else 0.
  */
 int inkling_rel_attn_build_tables_step(
