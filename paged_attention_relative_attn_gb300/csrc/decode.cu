@@ -988,10 +988,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm)
     // scales replace the maxima in comb_m, 1 / Ls and the output row index go
     // to comb_l (the thread reads its row's l values before it overwrites
     // them).
-    // MULTI, M = -inf: no key of this item is visible to the row (a split may
-    // lie wholly past a row's position): an empty result, o = 0 and lse = -inf,
-    // which the merge weighs at zero.  With one token every key of an item is
-    // visible to its rows.
+    // M = -inf: the row sees no key of this item (MULTI: a split may lie wholly past its position), or all of
+    // those have the bias -inf: an empty result, o = 0 and lse = -inf, which the merge weighs at zero.
     if (tid < NRi) {
       const int h = tid;
       float M = -INFINITY;
@@ -1000,12 +998,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm)
       float sc[kCombSlots], Ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kCombSlots; ++w) {
-        sc[w] = (!MULTI || M > -INFINITY) ? ex2(comb_m[w * HP + h] - M) : 0.f;
+        sc[w] = M > -INFINITY ? ex2(comb_m[w * HP + h] - M) : 0.f;
         Ls = fmaf(sc[w], comb_l[w * HP + h], Ls);
       }
-      float lse;
-      if constexpr (MULTI) lse = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
-      else lse = (M + log2f(Ls)) * kLn2;
+      const float lse = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
       const size_t row = out_row(h);
       if (final_out) {
         if (p.lse_out) p.lse_out[row] = lse;
@@ -1014,8 +1010,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm)
       }
 #pragma unroll
       for (int w = 0; w < kCombSlots; ++w) comb_m[w * HP + h] = sc[w];
-      if constexpr (MULTI) comb_l[h] = Ls == 0.f ? 0.f : 1.f / Ls;
-      else comb_l[h] = 1.f / Ls;
+      comb_l[h] = Ls == 0.f ? 0.f : 1.f / Ls;
       reinterpret_cast<int*>(comb_l)[HP + h] = (int)row;
     }
     named_bar_sync(1, kConsumerThreads);
