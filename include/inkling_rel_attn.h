@@ -17,7 +17,8 @@
  *   lse[t, h]    = log(sum over visible j of exp(s_j))          (natural log)
  *
  * A query with no visible key (a sequence of length 0) gets out = 0 and
- * lse = -inf.  The local layers of the model use window 512 with 16 KV heads,
+ * lse = -inf, and so does one whose visible scores are all -inf (a bias of -inf
+ * is a mask).  A NaN among a query's scores makes its out and lse NaN.  The local layers of the model use window 512 with 16 KV heads,
  * the global layers a full causal mask (window <= 0) with 8 KV heads; the
  * bias table rel_logits has a static shape [tokens, H_q, R] (TensorRT-LLM
  * PR #17062, "Implementation": that is what makes decode graph-capturable).
@@ -189,7 +190,8 @@ size_t inkling_rel_attn_decode_multi_workspace_size(int32_t B, int32_t q_len,
  * cu_seqlens_q[b+1]-1.  They are the LAST q_len_b = cu_seqlens_q[b+1] -
  * cu_seqlens_q[b] tokens of a sequence whose seq_lens[b] keys (cached prefix
  * plus this chunk) are all in the cache, so query i sits at position
- * p = seq_lens[b] - q_len_b + i.
+ * p = seq_lens[b] - q_len_b + i.  A NaN or an infinity in V can reach queries of the same
+ * 128 tokens that do not see its key (their weight 0 times it).
  *
  *   q            bf16 [T, H_q, D]
  *   cu_seqlens_q int32 [B + 1], non-decreasing, cu_seqlens_q[0] = 0,
@@ -605,8 +607,9 @@ size_t inkling_rel_attn_prefill_q8_workspace_size(int32_t B, int32_t max_q_len,
  * before build_tables, which then gets their length as 0 (it would put
  * a shared page on the stack).  The calls work on page ids: one set of tables serves
  * every pool that it is for, bf16, 4-bit or 8-bit.  Results depend on the
- * arguments alone, not on timing; B <= 8192 (0: nothing is written), page_size,
- * page_table_stride, num_pages and the free stack as for build_tables.
+ * arguments alone, not on timing; B <= 8192, page_size,
+ * page_table_stride, num_pages and the free stack as for build_tables.  B = 0: fork_pages and
+ * release_pages write nothing, free_left neither; compact_pages orders the stack and writes an empty list.
  */
 
 /*

@@ -5,8 +5,11 @@
 // group's (token, query head) pairs, at most 8, and its keys the visible range in
 // tiles of two 16-token blocks.  (More rows in two MMA columns would read K and V
 // once for them, but need twice the accumulators: over the 4-bit cache 64 query heads
-// over 4 KV heads took 116 us so and 95 us as two items, the second of which finds K
-// and V in L2.)
+// over 4 KV heads took 116 us so and 95 us as two items.)  The items of a head come one
+// after the other, each over all its keys: a later one finds K and V in L2 where what the
+// thread blocks read between its visits to a key stays within it, as with a window of 512 keys,
+// and reads them from HBM again over long ranges (8-bit, 32 sequences to 32768 keys, 6 query
+// heads per KV head: 181 us for one token, 343 for 2, 678 for 4, each an item of its own).
 // All tiles of the batch, in (sequence, head, group, key) order, are cut into one
 // equal run per thread block of a grid that fills the GPU, so every one streams the
 // same bytes whatever the lengths are.  An item inside a run is finished there; the
@@ -19,7 +22,8 @@
 // contiguous) into a ring of slots by bulk copy, a lane per tile; the ring runs
 // across items, so the next one streams in while the current one is finished.  The
 // other prepares the items (q as operands, bias pointers and positions per lane),
-// three ahead; the 8-bit cache has a third for the sums of items of several tokens.  Consumer warp w takes the ring's tiles w, w + 4, ... with an online
+// three ahead; the 8-bit cache has a third for the sums of items of several tokens.
+// Consumer warp w takes the ring's tiles w, w + 4, ... with an online
 // softmax of its own; at the item's end it leaves (m, l, O) in one of two
 // shared-memory buffers and goes on, and the preparing warp adds the parts up.  (One
 // producer, and the last consumer to leave its part adding them up: over the 4-bit
@@ -61,8 +65,8 @@ constexpr float kRunSlack = 5.5f;     // scores may exceed the exponent base by 
 constexpr int kRunW = 4;              // consumer warps
 constexpr int kRunCtas = 2;           // thread blocks per SM
 // Items of several tokens have up to 8 rows to add up, a warp's work of its own where the registers
-// allow it (8-bit, 64 sequences of 4 drafts: 57.3 us, by the preparing warp 62.5; items of one token,
-// with 3 rows, 36.6 and 35.7).
+// allow it (8-bit, 64 sequences of 4 drafts: 57.3 us, by the preparing warp 62.5, both before Q8Format::mark; items
+// of one token, with 3 rows, 36.6 and 35.7).
 template <class F, bool MULTI>
 constexpr bool run_joiner() {
   return F::kJoiner && MULTI;
