@@ -18,7 +18,8 @@
  *
  * A query with no visible key (a sequence of length 0) gets out = 0 and
  * lse = -inf, and so does one whose visible scores are all -inf (a bias of -inf
- * is a mask).  A NaN among a query's scores makes its out and lse NaN.  The local layers of the model use window 512 with 16 KV heads,
+ * is a mask).  A NaN among a query's scores makes its out and lse NaN.
+ *   The local layers of the model use window 512 with 16 KV heads,
  * the global layers a full causal mask (window <= 0) with 8 KV heads; the
  * bias table rel_logits has a static shape [tokens, H_q, R] (TensorRT-LLM
  * PR #17062, "Implementation": that is what makes decode graph-capturable).
@@ -370,7 +371,8 @@ int inkling_rel_attn_build_tables(
  * it: a sequence with fewer tokens than its rows is skipped by kv_append,
  * kv_conv_append (its convolution state too), prefill and prefill_q4
  * (INKLING_DEVERR_BAD_CHUNK), and gets out = 0, lse = -inf from the decode calls.
- * A staging pool for the convolution ahead of kv_append_q4 or kv_append_q8 has lengths of its own: the
+ * A staging pool for the convolution ahead of kv_append_q4 or kv_append_q8 has
+ * lengths of its own: the
  * step's new tokens where step_lens > 0, else 0.
  */
 int inkling_rel_attn_build_tables_step(
@@ -434,9 +436,9 @@ int inkling_rel_attn_kv_read_q4(
  * cache: the last q_len (1 .. 64) tokens of each sequence, q_len = 1 being plain
  * decode.  Same formula on the values x * s, same shapes, lengths and errors;
  * one more rule: a row all of whose visible scores are -inf gets out = 0, lse =
- * -inf.  A NaN in a row of the cache that a token sees makes its outputs NaN, in K out and lse, in V the
- * channels of out that have it, whatever the key's bias (-inf too) and weight (0 too; but for the
- * rule before).  Keys past a row's position or window, and places past a sequence's
+ * -inf.  A NaN in a row of the cache that a token sees makes its outputs NaN, in K out
+ * and lse, in V the channels of out that have it, whatever the key's bias (-inf too) and
+ * weight (0 too; but for the rule before).  Keys past a row's position or window, and places past a sequence's
  * end, may hold any bytes; page ids of pages wholly before every row's window are
  * not looked at.
  *   The work is cut over the GPU by the batch's lengths, read on the device:

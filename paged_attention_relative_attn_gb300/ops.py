@@ -655,7 +655,8 @@ def fork_pages(source, seq_lens, page_table, page_refs, free_pages, free_count, 
     place; free_pages [num_pages] int32, a stack of free_count [1] int32 pages.
     Returns (kv_lens [B], copy_src [B], copy_dst [B], free_left [1]), int32; pass them to
     avoid allocations.  kv_lens=seq_lens and free_left=free_count step the state in
-    place.  ``copy_pages(pools, copy_src, copy_dst)`` then copies the partial pages.
+    place.  ``copy_pages(pools, copy_src, copy_dst)`` then copies the partial pages.  A fork
+    for which there is no page, or that meets a page id that is none, stays empty.
     """
     if stream is not None:
         return _on_stream(stream, seq_lens, lambda: fork_pages(
